@@ -510,6 +510,160 @@ fasa_status fasa_dense_decode(const fasa_cache* cache, int32_t len, const void* 
                               void* out, void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /*
+ * Attention over a span of a cache: every slot, or a sliding window and the
+ * first tokens ("sinks"). These calls serve the layers that FASA does not
+ * (dense and windowed layers, prompts) and the caches it is compared with.
+ *
+ * A query at position p of a sequence whose slots 0 .. L-1 hold tokens sees
+ * slot t when t < L, t <= p, and one of: window == 0, t > p - window, t <
+ * n_sink. (The window counts the query's own position: with p = L the query's
+ * key is not cached and L - window + 1 is the first slot inside.) Slots count
+ * as positions here; after fasa_evict they no longer are, so use window 0
+ * then. Each query head of KV head g attends over the slots it sees:
+ *   out = sum_t softmax_t(q' . k[t] / sqrt(128)) v[t],
+ * and a query that sees no slot gets zeros. What the cache holds in slots
+ * that no query of the call's sequence sees is never used, whatever it is.
+ *
+ *  seq_len    : device [B] int32, L of each sequence, 0 .. max_seq_len (a
+ *               value outside is clamped and flagged FASA_ERR_BAD_INDEX).
+ *  q_pos      : device [B] int32, the position of each sequence's (first)
+ *               query, or NULL: see the calls. A negative position sees
+ *               nothing.
+ *  q_len      : fasa_attend_prompt only: device [B] int32, the queries of each
+ *               sequence, 0 .. n_q (clamped and flagged likewise), or NULL: n_q.
+ *  max_seq_len: host bound, 1 .. cache max_len.
+ *  window     : 0 (none) or the positions a query sees, >= 1.
+ *  n_sink     : first slots that stay visible, >= 0 (no effect without a window).
+ *  q_prerotated: 0: queries are pre-RoPE; 1: already rotated.
+ */
+typedef struct fasa_span {
+  const int32_t* seq_len;
+  const int32_t* q_pos;
+  const int32_t* q_len;
+  int32_t max_seq_len;
+  int32_t window;
+  int32_t n_sink;
+  int32_t q_prerotated;
+} fasa_span;
+
+/* Workspace bytes fasa_attend_decode needs (0 for invalid arguments); more
+ * with weights (with_mass != 0). */
+size_t fasa_attend_decode_workspace_bytes(const fasa_cache* cache, const fasa_span* span, int32_t with_mass);
+
+/*
+ * Attention of one new token per sequence over its span, contiguous (pages
+ * NULL) or paged. The visible slots of all rows are dealt to the GPU's CTAs
+ * in equal shares, so sequences of very different lengths finish together; a
+ * row that several CTAs share is joined by a second launch. Rows short enough
+ * for one CTA each (max_seq_len, or the window and the sinks, within 256
+ * slots) take one launch.
+ *
+ *  q_pos   : span->q_pos, or NULL: the query of sequence b sits at position
+ *            seq_len[b], as in fasa_decode_varlen. span->q_len is not read.
+ *  q       : [B][Hq][128] dtype.
+ *  out     : [B][Hq][128] dtype.
+ *  mass    : nullable; [B][Hkv][max_len] float32. Each visible slot's
+ *            attention weight, summed over the group's query heads, is added
+ *            to it: mass[b][g][t] += sum_h softmax_t(...). Other slots are left
+ *            as they are. This is what fasa_evict goes by.
+ *  workspace : at least fasa_attend_decode_workspace_bytes bytes, 256-byte
+ *            aligned; plain scratch (no initial value, nothing kept between
+ *            calls). Calls that overlap on the GPU must not share one.
+ *  Arithmetic: float32 logits, softmax statistics and sums; bf16 caches use
+ *  tensor-core products with the queries and the probabilities in two bf16
+ *  terms each (16 significant bits). Results do not depend on timing.
+ *  A page outside the pool is flagged FASA_ERR_BAD_INDEX and its slots are
+ *  left out. Errors: as fasa_decode_varlen; f32 caches are served too.
+ */
+fasa_status fasa_attend_decode(const fasa_cache* cache, const fasa_paged* pages, const fasa_span* span,
+                               const void* q, void* out, float* mass, void* workspace, size_t workspace_bytes,
+                               cudaStream_t stream);
+
+/* Workspace bytes fasa_attend_prompt needs (0 for invalid arguments). */
+size_t fasa_attend_prompt_workspace_bytes(const fasa_cache* cache, const fasa_span* span, int32_t n_q);
+
+/*
+ * The same attention for prompts: up to n_q queries per sequence, causal (and
+ * windowed) among themselves through their positions. The prompt's keys and
+ * values are in the cache already (append them first).
+ *
+ *  q_pos   : query j of sequence b sits at position q_pos[b] + j; NULL: the
+ *            queries are the sequence's last tokens, q_pos[b] = seq_len[b] -
+ *            q_len[b].
+ *  q, out  : [B][n_q][Hq][128] dtype; rows j >= q_len[b] are not read and their
+ *            output is left as it is.
+ *  workspace : at least fasa_attend_prompt_workspace_bytes bytes, 256-byte
+ *            aligned, as for fasa_attend_decode.
+ *  Errors: as fasa_attend_decode; n_q < 1 -> FASA_ERR_INVALID_ARG; n_q >
+ *  FASA_MAX_LEN -> FASA_ERR_UNSUPPORTED.
+ */
+fasa_status fasa_attend_prompt(const fasa_cache* cache, const fasa_paged* pages, const fasa_span* span,
+                               const void* q, int32_t n_q, void* out, void* workspace, size_t workspace_bytes,
+                               cudaStream_t stream);
+
+/*
+ * Eviction from a cache by accumulated attention weight. Of the L =
+ * seq_len[b] slots of every (b, g), n = min(L, budget) stay: those whose
+ * token is among the first n_sink positions (slot_pos < n_sink) or the
+ * n_recent newest (slot_pos > cur_pos[b] - n_recent), and of the others those
+ * with the largest mass, equal ones to the lower slot (-0.0 counts as +0.0).
+ * The kept rows of K, V and the sketch, their mass and slot_pos end up in
+ * slots 0 .. n-1: a kept slot below the budget keeps its place, and the i-th
+ * kept slot at or behind the budget (ascending) moves to the i-th evicted
+ * slot below it. So only rows behind the budget move, and the heads of a
+ * sequence keep different tokens in the same slots. Slots are then no longer
+ * positions: append with fasa_append_kv_at, attend with window 0, give
+ * q_pos, and decode with the query's own position (fasa_decode) or rotated
+ * queries (fasa_decode_varlen, fasa_decode_paged).
+ *
+ *  seq_len, cur_pos : device [B] int32 each; L (0 .. max_seq_len, clamped and
+ *            flagged) and the newest token's position.
+ *  mass, slot_pos : [B][Hkv][max_len] float32 (finite) and int32, device.
+ *  mass_out, slot_pos_out : the same shape; each either the input itself (in
+ *            place) or memory apart from it. Entries 0 .. n-1 of a row are
+ *            written, the others left.
+ *  len_out : device [B] int32, n of every sequence; not seq_len itself.
+ *  budget >= 1 and n_sink + n_recent <= budget; max_seq_len <= FASA_MAX_LEN.
+ *  pages   : NULL, or a paged cache whose pages belong to one sequence each.
+ *            A move from or to a page outside the pool is flagged
+ *            FASA_ERR_BAD_INDEX and left out.
+ *  workspace : at least fasa_evict_workspace_bytes bytes, 256-byte aligned,
+ *            plain scratch.
+ *  Errors: bad sizes or pointers -> FASA_ERR_INVALID_ARG; max_seq_len beyond
+ *  the cache -> FASA_ERR_CAPACITY; a short workspace -> FASA_ERR_WORKSPACE.
+ */
+typedef struct fasa_evict_desc {
+  const int32_t* seq_len;
+  const int32_t* cur_pos;
+  int32_t max_seq_len;
+  int32_t budget;
+  int32_t n_sink;
+  int32_t n_recent;
+} fasa_evict_desc;
+
+size_t fasa_evict_workspace_bytes(const fasa_cache* cache, const fasa_evict_desc* desc);
+
+fasa_status fasa_evict(const fasa_cache* cache, const fasa_paged* pages, const fasa_evict_desc* desc,
+                       const float* mass, const int32_t* slot_pos, float* mass_out, int32_t* slot_pos_out,
+                       int32_t* len_out, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * fasa_append_kv into slots that are not the tokens' positions (a cache after
+ * fasa_evict), contiguous (pages NULL) or paged: token i of sequence b is
+ * rotated at position pos0[b] + i and stored in slot slot0[b] + i of every KV
+ * head. With slot0 equal to pos0 the rows are those of fasa_append_kv.
+ *  slot0, pos0 : device [B] int32. A sequence whose slots leave 0 ..
+ *            max_len-1, or whose positions leave the int32 range, is skipped
+ *            and flagged FASA_ERR_BAD_INDEX.
+ *  slot_pos, mass : nullable; [B][Hkv][max_len] int32 and float32: the new
+ *            slots' positions are set and their weights zeroed.
+ *  Errors: as fasa_append_kv_paged.
+ */
+fasa_status fasa_append_kv_at(const fasa_cache* cache, const fasa_paged* pages, const void* k_new,
+                              const void* v_new, int32_t n_new, const int32_t* slot0, const int32_t* pos0,
+                              int32_t* slot_pos, float* mass, cudaStream_t stream);
+
+/*
  * Synchronizes the current device, then returns FASA_OK or the first
  * device-side problem recorded since the status was last cleared
  * (FASA_ERR_BAD_INDEX, FASA_ERR_TIMEOUT); clears it when clear != 0.

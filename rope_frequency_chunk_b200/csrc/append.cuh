@@ -11,7 +11,9 @@
 // consecutive (b, g) rows. cos/sin of a token block are computed once in
 // float64 and reused across the CTA's heads (recomputed per sequence when
 // every sequence appends at its own position). Slots are addressed through
-// a PageMap, so the same kernel fills contiguous and paged caches.
+// a PageMap, so the same kernel fills contiguous and paged caches. After an
+// eviction slots are no longer positions: the first slot then comes apart
+// from the first position, and the slots' positions and weights are set too.
 #pragma once
 
 #include "fasa_device.cuh"
@@ -37,6 +39,9 @@ struct AppendParams {
   int32_t stride;
   int32_t heads_per_cta;
   const int32_t* pos0v;  // [B] each sequence's first new position, or null: pos0 for all
+  const int32_t* slot0v; // [B] each sequence's first new slot, or null: slots are positions
+  int32_t* slot_pos;     // [B*Hkv][max_len] the new slots' positions, or null
+  float* mass;           // [B*Hkv][max_len] zeroed at the new slots, or null
   PageMap pm;            // paged pools, or pm.table null: [B*Hkv][max_len] planes
   double theta[kNFC];    // base^(-2i/128), computed on the host in float64
 };
@@ -70,10 +75,12 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
 
   for (int row = row0; row < row1; ++row) {
     const int b = row / p.n_kv_heads, g = row % p.n_kv_heads;
-    int pos = p.pos0;
+    int pos = p.pos0, slot = p.pos0;
     if (p.pos0v) {
       pos = __ldg(p.pos0v + b);
-      if (pos < 0 || (int64_t)pos + p.n_new > p.max_len) {  // block-uniform: skip the row
+      slot = p.slot0v ? __ldg(p.slot0v + b) : pos;
+      // block-uniform: skip the row
+      if (pos < 0 || slot < 0 || (int64_t)slot + p.n_new > p.max_len || (int64_t)pos + p.n_new > INT32_MAX) {
         if (tid == 0 && blockIdx.x == 0) flag_status(FASA_ERR_BAD_INDEX);
         continue;
       }
@@ -85,8 +92,14 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
     }
     __syncthreads();  // s_cos ready; previous row done with s_row / s_dom / s_dst
     if (tid < ntok) {
-      const int t = pos + tok0 + tid;
-      s_dst[tid] = p.pm.table ? (int64_t)paged_row(p.pm, b, g, t) : (int64_t)row * p.max_len + t;
+      const int t = slot + tok0 + tid;
+      const int64_t at = (int64_t)row * p.max_len + t;
+      const int64_t dst = p.pm.table ? (int64_t)paged_row(p.pm, b, g, t) : at;
+      s_dst[tid] = dst;
+      if (dst >= 0) {
+        if (p.slot_pos) p.slot_pos[at] = pos + tok0 + tid;
+        if (p.mass) p.mass[at] = 0.0f;
+      }
     }
     if (tid < p.n_dom) {
       int d = p.dom_idx[g * p.n_dom + tid];

@@ -19,6 +19,8 @@
 #include "attend_tc.cuh"
 #include "decode_wide.cuh"
 #include "calibrate.cuh"
+#include "span.cuh"
+#include "evict.cuh"
 
 using namespace fasa;
 
@@ -738,7 +740,8 @@ DenseWs dense_layout(const fasa_cache* c, int32_t len) {
 
 // The append kernel's launch: every sequence at pos0, or at pos0v[b].
 fasa_status launch_append(const fasa_cache* c, const void* k_new, const void* v_new, int32_t n_new, int32_t pos0,
-                          const int32_t* pos0v, const fasa_paged* pg, const DevInfo& d, cudaStream_t stream) {
+                          const int32_t* pos0v, const fasa_paged* pg, const DevInfo& d, cudaStream_t stream,
+                          const int32_t* slot0v = nullptr, int32_t* slot_pos = nullptr, float* mass = nullptr) {
   AppendParams p{};
   p.k_new = k_new;
   p.v_new = v_new;
@@ -752,6 +755,9 @@ fasa_status launch_append(const fasa_cache* c, const void* k_new, const void* v_
   p.n_new = n_new;
   p.pos0 = pos0;
   p.pos0v = pos0v;
+  p.slot0v = slot0v;
+  p.slot_pos = slot_pos;
+  p.mass = mass;
   p.pm = page_map(c, pg);
   p.n_dom = c->n_dom;
   p.stride = c->sketch_stride;
@@ -1458,3 +1464,5 @@ fasa_status fasa_device_status(int32_t clear) {
 }
 
 }  // extern "C"
+
+#include "span_host.cuh"

@@ -1,0 +1,289 @@
+// Host side of the span attention (fasa_attend_decode, fasa_attend_prompt),
+// the eviction (fasa_evict) and the append to slots (fasa_append_kv_at):
+// argument checks before any launch, launch shapes, workspaces. Included by
+// fasa.cu, whose helpers it uses.
+#pragma once
+
+namespace {
+
+fasa_status check_span(const fasa_cache* c, const fasa_span* sp) {
+  if (sp == nullptr || !aligned(sp->seq_len, 4)) return FASA_ERR_INVALID_ARG;
+  if (sp->q_pos != nullptr && !aligned(sp->q_pos, 4)) return FASA_ERR_INVALID_ARG;
+  if (sp->q_len != nullptr && !aligned(sp->q_len, 4)) return FASA_ERR_INVALID_ARG;
+  if (sp->max_seq_len < 1 || sp->window < 0 || sp->n_sink < 0 || (sp->q_prerotated != 0 && sp->q_prerotated != 1))
+    return FASA_ERR_INVALID_ARG;
+  if (sp->max_seq_len > c->max_len) return FASA_ERR_CAPACITY;
+  return FASA_OK;
+}
+
+// Units of kSpanUnit slots that a row can have: its visible slots' units, the
+// window's cut at both ends.
+int64_t span_max_units(const fasa_span* sp) {
+  int64_t n = ceil_div(sp->max_seq_len, kSpanUnit);
+  if (sp->window > 0)
+    n = std::min<int64_t>(n, ceil_div(sp->n_sink, kSpanUnit) + ceil_div(sp->window, kSpanUnit) + 1);
+  return n;
+}
+
+// Rows of up to this many units are one CTA's work each: no partials, and no
+// second launch to join them.
+constexpr int kSpanWholeUnits = 4;
+constexpr int kSpanMaxPerSm = 4;  // resident CTAs per SM, an upper bound
+
+struct SpanWs {
+  int64_t max_cta;  // CTAs the units can be dealt to, 0 when every row is one CTA's
+  int64_t ld_logits;
+  size_t part, rstat, logits, total;
+};
+SpanWs span_layout(const fasa_cache* c, const fasa_span* sp, bool with_mass) {
+  SpanWs w;
+  const int64_t rows = (int64_t)c->batch * c->n_kv_heads, units = span_max_units(sp);
+  const int64_t G = c->n_q_heads / c->n_kv_heads;
+  w.max_cta = units <= kSpanWholeUnits ? 0 : std::min<int64_t>((int64_t)kAssumedMaxSms * kSpanMaxPerSm, rows * units);
+  w.ld_logits = ((int64_t)sp->max_seq_len + 31) / 32 * 32;
+  w.part = 0;
+  w.rstat = al256((size_t)(2 * w.max_cta * (kSpanHead + G * kD)) * 4);
+  w.logits = w.rstat + (with_mass ? al256((size_t)(rows * 2 * G) * 4) : 0);
+  w.total = w.logits + (with_mass ? al256((size_t)(rows * G * w.ld_logits) * 4) : 0);
+  return w;
+}
+
+void span_fill(SpanParams& p, const fasa_cache* c, const fasa_paged* pg, const fasa_span* sp, const void* q,
+               void* out, int32_t n_q) {
+  p.k = c->k;
+  p.v = c->v;
+  p.q = q;
+  p.out = out;
+  p.seq_len = sp->seq_len;
+  p.q_pos = sp->q_pos;
+  p.q_len = sp->q_len;
+  p.max_len = c->max_len;
+  p.max_seq_len = sp->max_seq_len;
+  p.window = sp->window;
+  p.n_sink = sp->n_sink;
+  p.q_prerot = sp->q_prerotated;
+  p.n_q = n_q;
+  p.batch = c->batch;
+  p.n_kv_heads = c->n_kv_heads;
+  p.group = c->n_q_heads / c->n_kv_heads;
+  p.pm = page_map(c, pg);
+  fill_theta(p.turns, c->rope_base);
+  for (int i = 0; i < kNFC; ++i) p.turns[i] *= 0.15915494309189535;  // 1 / (2 pi)
+}
+
+struct SpanCc {
+  const void* fn;
+  void (*kern)(const SpanParams);
+};
+template <typename T>
+SpanCc span_cc_pick(int G) {
+  if (G == 1) return {(const void*)span_cc_kernel<T, 1>, span_cc_kernel<T, 1>};
+  if (G == 2) return {(const void*)span_cc_kernel<T, 2>, span_cc_kernel<T, 2>};
+  if (G <= 4) return {(const void*)span_cc_kernel<T, 4>, span_cc_kernel<T, 4>};
+  if (G <= 8) return {(const void*)span_cc_kernel<T, 8>, span_cc_kernel<T, 8>};
+  return {(const void*)span_cc_kernel<T, 16>, span_cc_kernel<T, 16>};
+}
+
+fasa_status span_cc_launch(SpanParams& p, int dtype, dim3 grid, cudaStream_t st) {
+  const SpanCc k = dtype == FASA_F32 ? span_cc_pick<float>(p.group) : span_cc_pick<__nv_bfloat16>(p.group);
+  return launch_pdl(k.kern, grid, kSpanThreads, 0, st, p);
+}
+
+fasa_status check_mass(const float* mass) { return aligned(mass, 4) ? FASA_OK : FASA_ERR_INVALID_ARG; }
+
+}  // namespace
+
+extern "C" {
+
+size_t fasa_attend_decode_workspace_bytes(const fasa_cache* c, const fasa_span* sp, int32_t with_mass) {
+  if (check_cache(c) != FASA_OK || check_span(c, sp) != FASA_OK) return 0;
+  return span_layout(c, sp, with_mass != 0).total + 256;
+}
+
+fasa_status fasa_attend_decode(const fasa_cache* c, const fasa_paged* pg, const fasa_span* sp, const void* q,
+                               void* out, float* mass, void* workspace, size_t workspace_bytes,
+                               cudaStream_t stream) {
+  fasa_status s = check_cache(c);
+  if (s != FASA_OK) return s;
+  if (pg != nullptr && (s = check_paged(c, pg)) != FASA_OK) return s;
+  if ((s = check_span(c, sp)) != FASA_OK) return s;
+  if (!aligned(q, 16) || !aligned(out, 16)) return FASA_ERR_INVALID_ARG;
+  if (mass != nullptr && (s = check_mass(mass)) != FASA_OK) return s;
+  const SpanWs w = span_layout(c, sp, mass != nullptr);
+  if (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < w.total + 256) return FASA_ERR_WORKSPACE;
+  DevInfo d;
+  if ((s = device_info(&d)) != FASA_OK) return s;
+  SpanParams p{};
+  span_fill(p, c, pg, sp, q, out, 1);
+  p.q_len = nullptr;
+  p.pos_at_len = 1;
+  const int rows = c->batch * c->n_kv_heads;
+  char* base = static_cast<char*>(workspace);
+  p.part = reinterpret_cast<float*>(base + w.part);
+  if (mass != nullptr) {
+    p.mass = mass;
+    p.mass_ld = c->max_len;
+    p.rstat = reinterpret_cast<float*>(base + w.rstat);
+    p.logits = reinterpret_cast<float*>(base + w.logits);
+    p.ld_logits = w.ld_logits;
+  }
+  const SpanCc k = c->dtype == FASA_F32 ? span_cc_pick<float>(p.group) : span_cc_pick<__nv_bfloat16>(p.group);
+  dim3 grid(1, (unsigned)rows, 1);
+  if (w.max_cta > 0) {
+    int per_sm = 0;
+    if ((s = cached_int(k.fn, 7, &per_sm, [&](int* v) {
+           return cuda_status(cudaOccupancyMaxActiveBlocksPerMultiprocessor(v, k.fn, kSpanThreads, 0));
+         })) != FASA_OK)
+      return s;
+    per_sm = std::min(std::max(per_sm, 1), kSpanMaxPerSm);
+    p.n_cta = (int)std::min<int64_t>((int64_t)per_sm * d.sms, w.max_cta);
+    grid = dim3((unsigned)p.n_cta, 1, 1);
+  }
+  if ((s = span_cc_launch(p, c->dtype, grid, stream)) != FASA_OK) return s;
+  if (p.n_cta == 0 && mass == nullptr) return FASA_OK;
+  unsigned blocks = 0;
+  if (mass != nullptr)
+    blocks = (unsigned)std::max<int64_t>(
+        1, std::min<int64_t>(ceil_div(sp->max_seq_len, kSpanMassSlots), ceil_div(4LL * d.sms, rows)));
+  const dim3 mgrid((unsigned)rows, (unsigned)p.group + blocks, 1);
+  return c->dtype == FASA_F32 ? launch_pdl(span_merge_kernel<float>, mgrid, kSpanThreads, 0, stream, p)
+                              : launch_pdl(span_merge_kernel<__nv_bfloat16>, mgrid, kSpanThreads, 0, stream, p);
+}
+
+size_t fasa_attend_prompt_workspace_bytes(const fasa_cache* c, const fasa_span* sp, int32_t n_q) {
+  if (check_cache(c) != FASA_OK || check_span(c, sp) != FASA_OK || n_q < 1) return 0;
+  return 256;
+}
+
+fasa_status fasa_attend_prompt(const fasa_cache* c, const fasa_paged* pg, const fasa_span* sp, const void* q,
+                               int32_t n_q, void* out, void* workspace, size_t workspace_bytes,
+                               cudaStream_t stream) {
+  fasa_status s = check_cache(c);
+  if (s != FASA_OK) return s;
+  if (pg != nullptr && (s = check_paged(c, pg)) != FASA_OK) return s;
+  if ((s = check_span(c, sp)) != FASA_OK) return s;
+  if (n_q < 1 || !aligned(q, 16) || !aligned(out, 16)) return FASA_ERR_INVALID_ARG;
+  if (n_q > FASA_MAX_LEN) return FASA_ERR_UNSUPPORTED;
+  const size_t need = fasa_attend_prompt_workspace_bytes(c, sp, n_q);
+  if (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < need) return FASA_ERR_WORKSPACE;
+  DevInfo d;
+  if ((s = device_info(&d)) != FASA_OK) return s;
+  SpanParams p{};
+  span_fill(p, c, pg, sp, q, out, n_q);
+  const dim3 grid((unsigned)n_q, (unsigned)(c->batch * c->n_kv_heads), 1);
+  return span_cc_launch(p, c->dtype, grid, stream);
+}
+
+fasa_status fasa_append_kv_at(const fasa_cache* c, const fasa_paged* pg, const void* k_new, const void* v_new,
+                              int32_t n_new, const int32_t* slot0, const int32_t* pos0, int32_t* slot_pos,
+                              float* mass, cudaStream_t stream) {
+  fasa_status s = check_cache(c);
+  if (s != FASA_OK) return s;
+  if (pg != nullptr && (s = check_paged(c, pg)) != FASA_OK) return s;
+  if (n_new < 0 || !aligned(slot0, 4) || !aligned(pos0, 4)) return FASA_ERR_INVALID_ARG;
+  if (slot_pos != nullptr && !aligned(slot_pos, 4)) return FASA_ERR_INVALID_ARG;
+  if (mass != nullptr && !aligned(mass, 4)) return FASA_ERR_INVALID_ARG;
+  if (n_new > c->max_len) return FASA_ERR_CAPACITY;
+  if (n_new == 0) return FASA_OK;
+  if (!aligned(k_new, 16) || !aligned(v_new, 16)) return FASA_ERR_INVALID_ARG;
+  DevInfo d;
+  if ((s = device_info(&d)) != FASA_OK) return s;
+  return launch_append(c, k_new, v_new, n_new, 0, pos0, pg, d, stream, slot0, slot_pos, mass);
+}
+
+}  // extern "C"
+
+namespace {
+
+fasa_status check_evict(const fasa_cache* c, const fasa_evict_desc* e) {
+  if (e == nullptr || !aligned(e->seq_len, 4) || !aligned(e->cur_pos, 4)) return FASA_ERR_INVALID_ARG;
+  if (e->max_seq_len < 1 || e->budget < 1 || e->n_sink < 0 || e->n_recent < 0) return FASA_ERR_INVALID_ARG;
+  if ((int64_t)e->n_sink + e->n_recent > e->budget) return FASA_ERR_INVALID_ARG;
+  if (e->max_seq_len > c->max_len) return FASA_ERR_CAPACITY;
+  if (e->max_seq_len > FASA_MAX_LEN) return FASA_ERR_UNSUPPORTED;
+  return FASA_OK;
+}
+
+// A kept slot behind the budget fills a hole before it: at most the smaller
+// of the two sides.
+int32_t evict_max_moves(const fasa_evict_desc* e) {
+  return std::max(1, std::min(e->budget, e->max_seq_len - std::min(e->budget, e->max_seq_len)));
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t fasa_evict_workspace_bytes(const fasa_cache* c, const fasa_evict_desc* e) {
+  if (check_cache(c) != FASA_OK || check_evict(c, e) != FASA_OK) return 0;
+  return al256((size_t)c->batch * c->n_kv_heads * 2 * evict_max_moves(e) * 4);
+}
+
+fasa_status fasa_evict(const fasa_cache* c, const fasa_paged* pg, const fasa_evict_desc* e, const float* mass,
+                       const int32_t* slot_pos, float* mass_out, int32_t* slot_pos_out, int32_t* len_out,
+                       void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  fasa_status s = check_cache(c);
+  if (s != FASA_OK) return s;
+  if (pg != nullptr && (s = check_paged(c, pg)) != FASA_OK) return s;
+  if ((s = check_evict(c, e)) != FASA_OK) return s;
+  if (!aligned(mass, 4) || !aligned(slot_pos, 4) || !aligned(mass_out, 4) || !aligned(slot_pos_out, 4) ||
+      !aligned(len_out, 4) || len_out == e->seq_len)
+    return FASA_ERR_INVALID_ARG;
+  const size_t need = fasa_evict_workspace_bytes(c, e);
+  if (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < need) return FASA_ERR_WORKSPACE;
+  DevInfo d;
+  if ((s = device_info(&d)) != FASA_OK) return s;
+  EvictParams p{};
+  p.k = c->k;
+  p.v = c->v;
+  p.sketch = c->sketch;
+  p.seq_len = e->seq_len;
+  p.cur_pos = e->cur_pos;
+  p.mass = mass;
+  p.slot_pos = slot_pos;
+  p.mass_out = mass_out;
+  p.slot_pos_out = slot_pos_out;
+  p.len_out = len_out;
+  p.moves = static_cast<int32_t*>(workspace);
+  p.max_len = c->max_len;
+  p.max_seq_len = e->max_seq_len;
+  p.budget = e->budget;
+  p.n_sink = e->n_sink;
+  p.n_recent = e->n_recent;
+  p.n_kv_heads = c->n_kv_heads;
+  p.max_moves = evict_max_moves(e);
+  p.row16 = kD * elem_bytes(c->dtype) / 16;
+  p.sk16 = c->sketch_stride * elem_bytes(c->dtype) / 16;
+  p.pm = page_map(c, pg);
+  const int rows = c->batch * c->n_kv_heads;
+  // CTAs per row: enough for a CTA's share of the keys to fit, more while the
+  // rows leave SMs idle and a CTA's share stays above 2048 slots
+  int C = pow2ceil(ceil_div(e->max_seq_len, kEvMaxChunk));
+  while (C < kMaxCluster && (int64_t)rows * C * 2 <= d.sms && ceil_div(e->max_seq_len, 2 * C) >= 2048) C *= 2;
+  p.chunk = (int)(ceil_div(ceil_div(e->max_seq_len, C), 32) * 32);
+  const size_t smem = (size_t)(2 * kEvBins + p.chunk) * 4;
+  int set = 0;
+  if ((s = cached_int((const void*)evict_kernel, 1, &set, [&](int* v) {
+         cudaError_t er = cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (2 * kEvBins + kEvMaxChunk) * 4);
+         if (er == cudaSuccess) er = cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+         *v = 1;
+         return cuda_status(er);
+       })) != FASA_OK)
+    return s;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = dim3((unsigned)C, (unsigned)rows, 1);
+  cfg.blockDim = dim3(kEvThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)C;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cuda_status(cudaLaunchKernelEx(&cfg, evict_kernel, p));
+}
+
+}  // extern "C"

@@ -49,6 +49,17 @@ class fasa_paged(ctypes.Structure):
                 ("n_pages", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
+class fasa_span(ctypes.Structure):
+    _fields_ = [("seq_len", ctypes.c_void_p), ("q_pos", ctypes.c_void_p), ("q_len", ctypes.c_void_p),
+                ("max_seq_len", ctypes.c_int32), ("window", ctypes.c_int32), ("n_sink", ctypes.c_int32),
+                ("q_prerotated", ctypes.c_int32)]
+
+
+class fasa_evict_desc(ctypes.Structure):
+    _fields_ = [("seq_len", ctypes.c_void_p), ("cur_pos", ctypes.c_void_p), ("max_seq_len", ctypes.c_int32),
+                ("budget", ctypes.c_int32), ("n_sink", ctypes.c_int32), ("n_recent", ctypes.c_int32)]
+
+
 _lib = None
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
@@ -79,6 +90,16 @@ _SIGS = {
     "fasa_decode_static_scratch": (_I, [_CP, _I, _P, _I, _I, _P, _P, _P]),
     "fasa_dense_workspace_bytes": (ctypes.c_size_t, [_CP, _I]),
     "fasa_dense_decode": (_I, [_CP, _I, _P, _I, _P, _P, ctypes.c_size_t, _P]),
+    "fasa_attend_decode_workspace_bytes": (ctypes.c_size_t, [_CP, ctypes.POINTER(fasa_span), _I]),
+    "fasa_attend_decode": (_I, [_CP, ctypes.POINTER(fasa_paged), ctypes.POINTER(fasa_span), _P, _P, _P, _P,
+                                ctypes.c_size_t, _P]),
+    "fasa_attend_prompt_workspace_bytes": (ctypes.c_size_t, [_CP, ctypes.POINTER(fasa_span), _I]),
+    "fasa_attend_prompt": (_I, [_CP, ctypes.POINTER(fasa_paged), ctypes.POINTER(fasa_span), _P, _I, _P, _P,
+                                ctypes.c_size_t, _P]),
+    "fasa_evict_workspace_bytes": (ctypes.c_size_t, [_CP, ctypes.POINTER(fasa_evict_desc)]),
+    "fasa_evict": (_I, [_CP, ctypes.POINTER(fasa_paged), ctypes.POINTER(fasa_evict_desc), _P, _P, _P, _P, _P, _P,
+                        ctypes.c_size_t, _P]),
+    "fasa_append_kv_at": (_I, [_CP, ctypes.POINTER(fasa_paged), _P, _P, _I, _P, _P, _P, _P, _P]),
     "fasa_device_status": (_I, [_I]),
     "fasa_host_kv_pointer": (_I, [_P, ctypes.POINTER(ctypes.c_void_p)]),
     "fasa_set_decode_path": (_I, [_I]),
@@ -438,6 +459,198 @@ def fasa_decode_multi(cache: KVCache, length: int, q, q_pos0: int, k: int, out=N
                                    _ptr(idx_out), workspace.data_ptr(), workspace.numel(), _stream(stream)),
            "fasa_decode_multi")
     return out
+
+
+# ------------------------------------- spans, eviction, appends to slots
+
+class _on:
+    """Makes a tensor's device the current one for a call (the library
+    launches on the current device)."""
+
+    def __init__(self, t):
+        self.other = None
+        if t.device.index != torch.cuda.current_device():
+            self.other = torch.cuda.device(t.device)
+
+    def __enter__(self):
+        if self.other is not None:
+            self.other.__enter__()
+
+    def __exit__(self, *a):
+        if self.other is not None:
+            self.other.__exit__(*a)
+
+
+def _pages(cache):
+    """The block table's description of a PagedKVCache, None for a KVCache."""
+    return cache.pref() if isinstance(cache, PagedKVCache) else None
+
+
+def _per_seq(cache, t, name):
+    """Address of an int32 [B] device tensor, or None."""
+    if t is None:
+        return None
+    _dev(t, name, torch.int32)
+    if t.numel() != cache.batch:
+        raise ValueError(f"{name} must have one value per sequence ({cache.batch}), got {t.numel()}")
+    return t.data_ptr()
+
+
+def _per_slot(cache, t, name, dtype):
+    """Address of a [B, Hkv, max_len] device tensor, or None."""
+    if t is None:
+        return None
+    _dev(t, name, dtype)
+    if tuple(t.shape) != (cache.batch, cache.n_kv_heads, cache.max_len):
+        raise ValueError(f"{name} must be [B, Hkv, max_len] = "
+                         f"{[cache.batch, cache.n_kv_heads, cache.max_len]}, got {list(t.shape)}")
+    return t.data_ptr()
+
+
+def _span(cache, seq_len, max_seq_len, window, n_sink, q_pos, q_len, q_prerotated):
+    if seq_len is None:
+        raise TypeError("seq_len must be a CUDA tensor")
+    return fasa_span(_per_seq(cache, seq_len, "seq_len"), _per_seq(cache, q_pos, "q_pos"),
+                     _per_seq(cache, q_len, "q_len"), int(max_seq_len), int(window), int(n_sink),
+                     1 if q_prerotated else 0)
+
+
+def _bounds(max_seq_len, window=0, n_sink=0):
+    """A span description of host bounds only (sizes workspaces)."""
+    return fasa_span(16, None, None, int(max_seq_len), int(window), int(n_sink), 0)
+
+
+def _scratch(need, call, device):
+    if need == 0:
+        raise FasaError(1, call)
+    return torch.empty(need, dtype=torch.uint8, device=device)
+
+
+def fasa_attend_decode_workspace(cache, max_seq_len: int, mass: bool = False, device=None):
+    """A workspace for fasa_attend_decode up to this length, any window."""
+    dev = device if device is not None else cache.sketch.device
+    return _scratch(int(lib().fasa_attend_decode_workspace_bytes(cache.ref(), ctypes.byref(_bounds(max_seq_len)),
+                                                             1 if mass else 0)),
+                    "fasa_attend_decode_workspace_bytes", dev)
+
+
+def fasa_attend_decode(cache, seq_len, q, max_seq_len: int, window: int = 0, n_sink: int = 0, q_pos=None,
+                       q_prerotated: bool = False, mass=None, out=None, workspace=None, stream=None):
+    """Attention of one new token per sequence over all its cached slots, or
+    the last `window` positions and the first n_sink slots. cache: a KVCache
+    or a PagedKVCache; seq_len (and q_pos, default seq_len): int32 [B] on the
+    device. mass, when given, is float32 [B, Hkv, max_len]: every visible
+    slot's attention weight, summed over the group's heads, is added to it."""
+    _q(cache, q)
+    sp = _span(cache, seq_len, max_seq_len, window, n_sink, q_pos, None, q_prerotated)
+    if out is None:
+        out = torch.empty_like(q)
+    _same(_dev(out, "out", cache.dtype), q)
+    m = _per_slot(cache, mass, "mass", torch.float32)
+    if workspace is None:
+        workspace = fasa_attend_decode_workspace(cache, max_seq_len, mass is not None, q.device)
+    _dev(workspace, "workspace", torch.uint8)
+    with _on(q):
+        _check(lib().fasa_attend_decode(cache.ref(), _pages(cache), ctypes.byref(sp), q.data_ptr(), out.data_ptr(), m,
+                                        workspace.data_ptr(), workspace.numel(), _stream(stream)),
+               "fasa_attend_decode")
+    return out
+
+
+def _same(out, q):
+    if out.shape != q.shape:
+        raise ValueError(f"out must be {list(q.shape)}, got {list(out.shape)}")
+
+
+def fasa_attend_prompt_workspace(cache, n_q: int, max_seq_len: int, device=None):
+    """A workspace for fasa_attend_prompt up to this length, any window."""
+    dev = device if device is not None else cache.sketch.device
+    return _scratch(int(lib().fasa_attend_prompt_workspace_bytes(cache.ref(), ctypes.byref(_bounds(max_seq_len)), int(n_q))),
+                    "fasa_attend_prompt_workspace_bytes", dev)
+
+
+def fasa_attend_prompt(cache, seq_len, q, max_seq_len: int, window: int = 0, n_sink: int = 0, q_pos=None,
+                       q_len=None, q_prerotated: bool = False, out=None, workspace=None, stream=None):
+    """The attention of fasa_attend_decode for prompts: q [B, n_q, Hq, 128],
+    query j of sequence b at position q_pos[b] + j (default: the queries are
+    the sequence's last tokens). With q_len (int32 [B] on the device) sequence
+    b has q_len[b] queries; the other rows of out are left as they are."""
+    _dev(q, "q", cache.dtype)
+    if q.dim() != 4 or tuple(q.shape[::2]) != (cache.batch, cache.n_q_heads) or q.shape[3] != HEAD_DIM:
+        raise ValueError("q must be [B, n_q, Hq, 128]")
+    n_q = q.shape[1]
+    sp = _span(cache, seq_len, max_seq_len, window, n_sink, q_pos, q_len, q_prerotated)
+    if out is None:
+        out = torch.empty_like(q)
+    _same(_dev(out, "out", cache.dtype), q)
+    if workspace is None:
+        workspace = fasa_attend_prompt_workspace(cache, n_q, max_seq_len, q.device)
+    _dev(workspace, "workspace", torch.uint8)
+    with _on(q):
+        _check(lib().fasa_attend_prompt(cache.ref(), _pages(cache), ctypes.byref(sp), q.data_ptr(), n_q,
+                                        out.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream(stream)),
+               "fasa_attend_prompt")
+    return out
+
+
+def _evict_desc(cache, seq_len, cur_pos, max_seq_len, budget, n_sink, n_recent):
+    if seq_len is None or cur_pos is None:
+        raise TypeError("seq_len and cur_pos must be CUDA tensors")
+    return fasa_evict_desc(_per_seq(cache, seq_len, "seq_len"), _per_seq(cache, cur_pos, "cur_pos"),
+                           int(max_seq_len), int(budget), int(n_sink), int(n_recent))
+
+
+def fasa_evict_workspace(cache, max_seq_len: int, budget: int, device=None):
+    """A workspace for fasa_evict at these bounds."""
+    dev = device if device is not None else cache.sketch.device
+    d = fasa_evict_desc(16, 16, int(max_seq_len), int(budget), 0, 0)
+    return _scratch(int(lib().fasa_evict_workspace_bytes(cache.ref(), ctypes.byref(d))),
+                    "fasa_evict_workspace_bytes", dev)
+
+
+def fasa_evict(cache, seq_len, cur_pos, mass, slot_pos, max_seq_len: int, budget: int, n_sink: int = 0,
+               n_recent: int = 0, mass_out=None, slot_pos_out=None, len_out=None, workspace=None, stream=None):
+    """Keeps min(seq_len[b], budget) slots of every (b, KV head): the first
+    n_sink positions, the n_recent newest (cur_pos: int32 [B], the newest
+    token's position) and the slots of the largest mass; kept rows behind the
+    budget move into the holes before it. mass (float32) and slot_pos (int32)
+    are [B, Hkv, max_len], updated in place unless mass_out / slot_pos_out are
+    given. Returns the new lengths, int32 [B]."""
+    d = _evict_desc(cache, seq_len, cur_pos, max_seq_len, budget, n_sink, n_recent)
+    if mass is None or slot_pos is None:
+        raise TypeError("mass and slot_pos must be CUDA tensors")
+    mp = _per_slot(cache, mass, "mass", torch.float32)
+    sp = _per_slot(cache, slot_pos, "slot_pos", torch.int32)
+    mo = mp if mass_out is None else _per_slot(cache, mass_out, "mass_out", torch.float32)
+    so = sp if slot_pos_out is None else _per_slot(cache, slot_pos_out, "slot_pos_out", torch.int32)
+    if len_out is None:
+        len_out = torch.empty_like(seq_len)
+    lo = _per_seq(cache, len_out, "len_out")
+    if workspace is None:
+        workspace = fasa_evict_workspace(cache, max_seq_len, budget, seq_len.device)
+    _dev(workspace, "workspace", torch.uint8)
+    with _on(seq_len):
+        _check(lib().fasa_evict(cache.ref(), _pages(cache), ctypes.byref(d), mp, sp, mo, so, lo,
+                                workspace.data_ptr(), workspace.numel(), _stream(stream)), "fasa_evict")
+    return len_out
+
+
+def fasa_append_kv_at(cache, k_new, v_new, slot0, pos0, slot_pos=None, mass=None, stream=None) -> None:
+    """Append n_new tokens to every sequence b at slots slot0[b] .., rotated
+    at positions pos0[b] .. (int32 [B] on the device). slot_pos (int32) and
+    mass (float32), [B, Hkv, max_len], get the new slots' positions and zeros."""
+    _dev(k_new, "k_new", cache.dtype)
+    _dev(v_new, "v_new", cache.dtype)
+    n_new = k_new.shape[2]
+    if tuple(k_new.shape) != (cache.batch, cache.n_kv_heads, n_new, HEAD_DIM) or v_new.shape != k_new.shape:
+        raise ValueError("k_new, v_new must be [B, Hkv, n_new, 128]")
+    if slot0 is None or pos0 is None:
+        raise TypeError("slot0 and pos0 must be CUDA tensors")
+    s0, p0 = _per_seq(cache, slot0, "slot0"), _per_seq(cache, pos0, "pos0")
+    sp, m = _per_slot(cache, slot_pos, "slot_pos", torch.int32), _per_slot(cache, mass, "mass", torch.float32)
+    with _on(k_new):
+        _check(lib().fasa_append_kv_at(cache.ref(), _pages(cache), k_new.data_ptr(), v_new.data_ptr(), n_new, s0, p0,
+                                       sp, m, _stream(stream)), "fasa_append_kv_at")
 
 
 DECODE_AUTO, DECODE_FUSED, DECODE_STAGED = 0, 1, 2
