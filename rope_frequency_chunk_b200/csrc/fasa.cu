@@ -20,6 +20,7 @@
 #include "decode_wide.cuh"
 #include "calibrate.cuh"
 #include "span.cuh"
+#include "span_prompt.cuh"
 #include "evict.cuh"
 
 using namespace fasa;

@@ -429,7 +429,7 @@ __device__ __forceinline__ void span_cc_segment(const SpanParams& p, SpanCcSmem<
       O += f * sm.o[w][h][d];
     }
     if (whole) {
-      store_f(out + e, L > 0.0f ? O / L : 0.0f);
+      store_f(out + e, L == 0.0f ? 0.0f : O / L);
       if (d == 0 && p.rstat != nullptr) {
         p.rstat[row * 2 * G + h] = M;
         p.rstat[row * 2 * G + G + h] = L;
@@ -558,7 +558,7 @@ __global__ void __launch_bounds__(kSpanThreads) span_merge_kernel(const __grid_c
       O += s_o[w][tid];
       L += s_l[w];
     }
-    store_f(out + h * kD + tid, L > 0.0f ? O / L : 0.0f);
+    store_f(out + h * kD + tid, L == 0.0f ? 0.0f : O / L);
     return;
   }
   // the weights: every head's maximum and reciprocal sum, then the slots
@@ -599,7 +599,7 @@ __global__ void __launch_bounds__(kSpanThreads) span_merge_kernel(const __grid_c
       float w = 0.0f;
       for (int h = 0; h < G; ++h) {
         const float z = __ldcg(p.logits + ((int64_t)row * G + h) * p.ld_logits + t);
-        if (s_l[h] > 0.0f) w += exp2f(z - s_m[h]) / s_l[h];
+        if (s_l[h] != 0.0f) w += exp2f(z - s_m[h]) / s_l[h];
       }
       p.mass[row * p.mass_ld + t] += w;
     }

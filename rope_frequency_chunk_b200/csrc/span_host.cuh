@@ -89,6 +89,98 @@ fasa_status span_cc_launch(SpanParams& p, int dtype, dim3 grid, cudaStream_t st)
   return launch_pdl(k.kern, grid, kSpanThreads, 0, st, p);
 }
 
+// Rows of the K (and V) tensor: every (b, g) plane, or every page.
+int64_t span_rows(const fasa_cache* c, const fasa_paged* pg) {
+  return pg != nullptr ? (int64_t)pg->n_pages * c->n_kv_heads * pg->block_size
+                       : (int64_t)c->batch * c->n_kv_heads * c->max_len;
+}
+
+// The tensor-core kernels read K and V with TMA: bf16 caches in device
+// memory, rows within the 32-bit coordinates. Others take the CUDA-core one.
+bool span_tensor_cores(const fasa_cache* c, const fasa_paged* pg) {
+  return c->dtype == FASA_BF16 && span_rows(c, pg) < INT32_MAX && !host_resident(c->k) && !host_resident(c->v);
+}
+
+// A [n_rows][128] bf16 tensor read in boxes of box_rows x 64 elements, stored
+// for the 128-byte swizzle; rows out of range read as zeros.
+fasa_status span_map(CUtensorMap* m, const void* base, int64_t n_rows, int box_rows) {
+  static std::atomic<void*> encode{nullptr};
+  void* fn = encode.load(std::memory_order_acquire);
+  if (fn == nullptr) {
+    cudaDriverEntryPointQueryResult found;
+    const cudaError_t e = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &found);
+    if (e != cudaSuccess || found != cudaDriverEntryPointSuccess || fn == nullptr)
+      return cuda_status(e == cudaSuccess ? cudaErrorNotSupported : e);
+    encode.store(fn, std::memory_order_release);
+  }
+  const cuuint64_t dims[2] = {(cuuint64_t)kD, (cuuint64_t)n_rows};
+  const cuuint64_t strides[1] = {kD * 2};
+  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, es[2] = {1, 1};
+  const CUresult r = reinterpret_cast<decltype(&cuTensorMapEncodeTiled)>(fn)(
+      m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
+      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? FASA_OK : cuda_status(cudaErrorInvalidValue);
+}
+
+// Work items of a prompt call and the parts their blocks are cut into: one
+// part while the items fill half the SMs or more; else enough parts to fill
+// them, each with four blocks or more.
+struct PromptPlan {
+  int64_t tiles, items;  // per (b, g) row; of all rows and parts
+  int splits;
+  size_t bytes;
+};
+PromptPlan prompt_layout(const fasa_cache* c, const fasa_span* sp, int32_t n_q, int sms) {
+  PromptPlan w;
+  const int64_t G = c->n_q_heads / c->n_kv_heads, rows = (int64_t)c->batch * c->n_kv_heads;
+  w.tiles = ceil_div((int64_t)n_q * G, kPrRows);
+  int64_t blocks = ceil_div(sp->max_seq_len, kPrBlock);
+  if (sp->window > 0)
+    blocks = std::min<int64_t>(blocks, ceil_div(sp->n_sink, kPrBlock) +
+                                           ceil_div((int64_t)sp->window + ceil_div(kPrRows, G), kPrBlock) + 1);
+  const int64_t items = w.tiles * rows;
+  w.splits = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(sms / items, blocks / 4), kPrMaxSplits));
+  w.items = items * w.splits;
+  w.bytes = 256 + (w.splits > 1 ? (size_t)(w.items * kPrPart) * 4 : 0);
+  return w;
+}
+
+template <int TERMS>
+fasa_status launch_prompt_t(const PromptParams& p, int grid, cudaStream_t st) {
+  auto kern = span_prompt_kernel<TERMS>;
+  constexpr int smem = (int)PrSmem<TERMS>::kBytes;
+  int set = 0;
+  fasa_status s = cached_int((const void*)kern, 0, &set, [&](int* v) {
+    *v = 1;
+    return cuda_status(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  });
+  if (s != FASA_OK) return s;
+  return launch_pdl(kern, dim3((unsigned)grid, 1, 1), kPrThreads, smem, st, p);
+}
+
+fasa_status launch_prompt(const fasa_cache* c, const fasa_paged* pg, const fasa_span* sp, const void* q, int32_t n_q,
+                          void* out, void* workspace, const DevInfo& d, cudaStream_t st) {
+  PromptParams p{};
+  span_fill(p.s, c, pg, sp, q, out, n_q);
+  const PromptPlan w = prompt_layout(c, sp, n_q, std::min(d.sms, kAssumedMaxSms));
+  if (w.items > INT32_MAX / 2) return FASA_ERR_UNSUPPORTED;
+  p.n_items = (int32_t)w.items;
+  p.tiles_max = (int32_t)w.tiles;
+  p.splits = w.splits;
+  p.box_rows = pg != nullptr ? std::min(pg->block_size, kPrBlock) : kPrBlock;
+  p.n_rows = (int32_t)span_rows(c, pg);
+  p.part = static_cast<float*>(workspace);
+  fasa_status s;
+  if ((s = span_map(&p.map_k, c->k, p.n_rows, p.box_rows)) != FASA_OK) return s;
+  if ((s = span_map(&p.map_v, c->v, p.n_rows, p.box_rows)) != FASA_OK) return s;
+  const int grid = (int)std::min<int64_t>(w.items, d.sms);
+  s = p.s.q_prerot ? launch_prompt_t<1>(p, grid, st) : launch_prompt_t<2>(p, grid, st);
+  if (s != FASA_OK || w.splits == 1) return s;
+  const dim3 mgrid((unsigned)ceil_div((int64_t)n_q * p.s.group, 4), (unsigned)(c->batch * c->n_kv_heads), 1);
+  return launch_pdl(span_prompt_merge_kernel, mgrid, 128, 0, st, p);
+}
+
 fasa_status check_mass(const float* mass) { return aligned(mass, 4) ? FASA_OK : FASA_ERR_INVALID_ARG; }
 
 }  // namespace
@@ -152,7 +244,7 @@ fasa_status fasa_attend_decode(const fasa_cache* c, const fasa_paged* pg, const 
 
 size_t fasa_attend_prompt_workspace_bytes(const fasa_cache* c, const fasa_span* sp, int32_t n_q) {
   if (check_cache(c) != FASA_OK || check_span(c, sp) != FASA_OK || n_q < 1) return 0;
-  return 256;
+  return prompt_layout(c, sp, n_q, kAssumedMaxSms).bytes;
 }
 
 fasa_status fasa_attend_prompt(const fasa_cache* c, const fasa_paged* pg, const fasa_span* sp, const void* q,
@@ -168,6 +260,7 @@ fasa_status fasa_attend_prompt(const fasa_cache* c, const fasa_paged* pg, const 
   if (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < need) return FASA_ERR_WORKSPACE;
   DevInfo d;
   if ((s = device_info(&d)) != FASA_OK) return s;
+  if (span_tensor_cores(c, pg)) return launch_prompt(c, pg, sp, q, n_q, out, workspace, d, stream);
   SpanParams p{};
   span_fill(p, c, pg, sp, q, out, n_q);
   const dim3 grid((unsigned)n_q, (unsigned)(c->batch * c->n_kv_heads), 1);
