@@ -21,6 +21,7 @@
 #include "calibrate.cuh"
 #include "span.cuh"
 #include "span_prompt.cuh"
+#include "span_decode.cuh"
 #include "evict.cuh"
 
 using namespace fasa;

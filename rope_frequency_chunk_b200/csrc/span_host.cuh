@@ -101,9 +101,10 @@ bool span_tensor_cores(const fasa_cache* c, const fasa_paged* pg) {
   return c->dtype == FASA_BF16 && span_rows(c, pg) < INT32_MAX && !host_resident(c->k) && !host_resident(c->v);
 }
 
-// A [n_rows][128] bf16 tensor read in boxes of box_rows x 64 elements, stored
-// for the 128-byte swizzle; rows out of range read as zeros.
-fasa_status span_map(CUtensorMap* m, const void* base, int64_t n_rows, int box_rows) {
+// A [n_rows][128] bf16 tensor read in boxes of box_rows x 64 elements, or
+// (halves) of both 64-column halves of box_rows rows, stored for the 128-byte
+// swizzle; rows out of range read as zeros.
+fasa_status span_map(CUtensorMap* m, const void* base, int64_t n_rows, int box_rows, bool halves) {
   static std::atomic<void*> encode{nullptr};
   void* fn = encode.load(std::memory_order_acquire);
   if (fn == nullptr) {
@@ -113,11 +114,11 @@ fasa_status span_map(CUtensorMap* m, const void* base, int64_t n_rows, int box_r
       return cuda_status(e == cudaSuccess ? cudaErrorNotSupported : e);
     encode.store(fn, std::memory_order_release);
   }
-  const cuuint64_t dims[2] = {(cuuint64_t)kD, (cuuint64_t)n_rows};
-  const cuuint64_t strides[1] = {kD * 2};
-  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, es[2] = {1, 1};
+  const cuuint64_t dims[3] = {(cuuint64_t)(halves ? kD / 2 : kD), (cuuint64_t)n_rows, 2};
+  const cuuint64_t strides[2] = {kD * 2, kD};  // bytes: a row, half a row
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 2}, es[3] = {1, 1, 1};
   const CUresult r = reinterpret_cast<decltype(&cuTensorMapEncodeTiled)>(fn)(
-      m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
+      m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, halves ? 3 : 2, const_cast<void*>(base), dims, strides, box, es,
       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? FASA_OK : cuda_status(cudaErrorInvalidValue);
@@ -172,13 +173,39 @@ fasa_status launch_prompt(const fasa_cache* c, const fasa_paged* pg, const fasa_
   p.n_rows = (int32_t)span_rows(c, pg);
   p.part = static_cast<float*>(workspace);
   fasa_status s;
-  if ((s = span_map(&p.map_k, c->k, p.n_rows, p.box_rows)) != FASA_OK) return s;
-  if ((s = span_map(&p.map_v, c->v, p.n_rows, p.box_rows)) != FASA_OK) return s;
+  if ((s = span_map(&p.map_k, c->k, p.n_rows, p.box_rows, false)) != FASA_OK) return s;
+  if ((s = span_map(&p.map_v, c->v, p.n_rows, p.box_rows, false)) != FASA_OK) return s;
   const int grid = (int)std::min<int64_t>(w.items, d.sms);
   s = p.s.q_prerot ? launch_prompt_t<1>(p, grid, st) : launch_prompt_t<2>(p, grid, st);
   if (s != FASA_OK || w.splits == 1) return s;
   const dim3 mgrid((unsigned)ceil_div((int64_t)n_q * p.s.group, 4), (unsigned)(c->batch * c->n_kv_heads), 1);
   return launch_pdl(span_prompt_merge_kernel, mgrid, 128, 0, st, p);
+}
+
+// One token per sequence: the tensor-core kernel where it can read the cache,
+// else the CUDA-core one, over n_cta CTAs (0: one per row).
+struct SpanDecodeKernel {
+  const void* fn;
+  int smem;
+};
+SpanDecodeKernel span_decode_pick(int dtype, bool tc, int G) {
+  if (tc)
+    return G <= 8 ? SpanDecodeKernel{(const void*)span_decode_kernel<8>, SdSmem<8>::kBytes}
+                  : SpanDecodeKernel{(const void*)span_decode_kernel<16>, SdSmem<16>::kBytes};
+  return {dtype == FASA_F32 ? span_cc_pick<float>(G).fn : span_cc_pick<__nv_bfloat16>(G).fn, 0};
+}
+fasa_status launch_span_decode(const fasa_cache* c, const fasa_paged* pg, SpanParams& p, bool tc, dim3 grid,
+                               cudaStream_t st) {
+  if (!tc) return span_cc_launch(p, c->dtype, grid, st);
+  SpanDecodeParams q{};
+  q.s = p;
+  const int64_t n_rows = span_rows(c, pg);
+  fasa_status s;
+  if ((s = span_map(&q.map_k, c->k, n_rows, kSdRows, true)) != FASA_OK) return s;
+  if ((s = span_map(&q.map_v, c->v, n_rows, kSdRows, true)) != FASA_OK) return s;
+  grid = dim3(grid.x * grid.y, 1, 1);
+  return p.group <= 8 ? launch_pdl(span_decode_kernel<8>, grid, kSpanThreads, SdSmem<8>::kBytes, st, q)
+                      : launch_pdl(span_decode_kernel<16>, grid, kSpanThreads, SdSmem<16>::kBytes, st, q);
 }
 
 fasa_status check_mass(const float* mass) { return aligned(mass, 4) ? FASA_OK : FASA_ERR_INVALID_ARG; }
@@ -219,19 +246,23 @@ fasa_status fasa_attend_decode(const fasa_cache* c, const fasa_paged* pg, const 
     p.logits = reinterpret_cast<float*>(base + w.logits);
     p.ld_logits = w.ld_logits;
   }
-  const SpanCc k = c->dtype == FASA_F32 ? span_cc_pick<float>(p.group) : span_cc_pick<__nv_bfloat16>(p.group);
+  const bool tc = span_tensor_cores(c, pg);
+  const SpanDecodeKernel k = span_decode_pick(c->dtype, tc, p.group);
+  int per_sm = 0;
+  if ((s = cached_int(k.fn, 7, &per_sm, [&](int* v) {
+         cudaError_t e = cudaSuccess;
+         if (k.smem > 0) e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
+         if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(v, k.fn, kSpanThreads, (size_t)k.smem);
+         return cuda_status(e);
+       })) != FASA_OK)
+    return s;
+  per_sm = std::min(std::max(per_sm, 1), kSpanMaxPerSm);
   dim3 grid(1, (unsigned)rows, 1);
   if (w.max_cta > 0) {
-    int per_sm = 0;
-    if ((s = cached_int(k.fn, 7, &per_sm, [&](int* v) {
-           return cuda_status(cudaOccupancyMaxActiveBlocksPerMultiprocessor(v, k.fn, kSpanThreads, 0));
-         })) != FASA_OK)
-      return s;
-    per_sm = std::min(std::max(per_sm, 1), kSpanMaxPerSm);
     p.n_cta = (int)std::min<int64_t>((int64_t)per_sm * d.sms, w.max_cta);
     grid = dim3((unsigned)p.n_cta, 1, 1);
   }
-  if ((s = span_cc_launch(p, c->dtype, grid, stream)) != FASA_OK) return s;
+  if ((s = launch_span_decode(c, pg, p, tc, grid, stream)) != FASA_OK) return s;
   if (p.n_cta == 0 && mass == nullptr) return FASA_OK;
   unsigned blocks = 0;
   if (mass != nullptr)
