@@ -57,10 +57,22 @@ struct EvictParams {
 
 constexpr uint32_t kEvHeld = 0xFFFFFFFFu;
 
-// Copies `n` 16-byte vectors of pool rows src -> dst with one warp.
-__device__ __forceinline__ void evict_copy(void* pool, int64_t src, int64_t dst, int n, int lane) {
+// Moves of one warp at a time: their rows are all in flight together.
+constexpr int kEvBatch = 8;
+
+// Copies `n` 16-byte vectors of each of the warp's rows rs[i] -> rd[i] (-1: none).
+__device__ __forceinline__ void evict_copy(void* pool, const int (&rs)[kEvBatch], const int (&rd)[kEvBatch],
+                                           int n, int lane) {
   uint4* base = static_cast<uint4*>(pool);
-  for (int c = lane; c < n; c += 32) base[dst * n + c] = base[src * n + c];
+  for (int c = lane; c < n; c += 32) {
+    uint4 x[kEvBatch];
+#pragma unroll
+    for (int i = 0; i < kEvBatch; ++i)
+      if (rs[i] >= 0) x[i] = __ldcs(base + (int64_t)rs[i] * n + c);
+#pragma unroll
+    for (int i = 0; i < kEvBatch; ++i)
+      if (rs[i] >= 0) base[(int64_t)rd[i] * n + c] = x[i];
+  }
 }
 
 __global__ void __launch_bounds__(kEvThreads) evict_kernel(const __grid_constant__ EvictParams p) {
@@ -125,7 +137,9 @@ __global__ void __launch_bounds__(kEvThreads) evict_kernel(const __grid_constant
       const int per = bins / C;  // this CTA adds up its share of the bins for everyone
       for (int i = tid; i < per; i += kEvThreads) {
         uint32_t s = 0;
+#pragma unroll 4
         for (int c = 0; c < C; ++c) s += cl.map_shared_rank(hist, c)[rank * per + i];
+#pragma unroll 4
         for (int c = 0; c < C; ++c) cl.map_shared_rank(tot, c)[rank * per + i] = s;
       }
       cl.sync();
@@ -245,15 +259,22 @@ __global__ void __launch_bounds__(kEvThreads) evict_kernel(const __grid_constant
   });
   if (C > 1) cl.sync(); else __syncthreads();  // every CTA's part of the lists is written
   const int n_warps = C * kEvWarps;
-  for (uint32_t i = rank * kEvWarps + warp; i < n_moves; i += n_warps) {
-    const int ts = src[i], td = dst[i];
-    if (lane == 0) {
+  for (uint32_t m0 = (rank * kEvWarps + warp) * kEvBatch; m0 < n_moves; m0 += n_warps * kEvBatch) {
+    int mine_s = -1, mine_d = -1;  // lane i < kEvBatch: the rows of move m0 + i
+    if (lane < kEvBatch && m0 + lane < n_moves) {
+      const int ts = src[m0 + lane], td = dst[m0 + lane];
       mass_o[td] = mass[ts];
       pos_o[td] = pos[ts];
+      mine_s = p.pm.table ? paged_row(p.pm, b, g, ts) : (int)(row * p.max_len + ts);
+      mine_d = p.pm.table ? paged_row(p.pm, b, g, td) : (int)(row * p.max_len + td);
+      if (mine_d < 0) mine_s = -1;  // a page outside the pool, flagged
     }
-    const int64_t rs = p.pm.table ? (int64_t)paged_row(p.pm, b, g, ts) : (int64_t)row * p.max_len + ts;
-    const int64_t rd = p.pm.table ? (int64_t)paged_row(p.pm, b, g, td) : (int64_t)row * p.max_len + td;
-    if (rs < 0 || rd < 0) continue;  // a page outside the pool, flagged
+    int rs[kEvBatch], rd[kEvBatch];
+#pragma unroll
+    for (int i = 0; i < kEvBatch; ++i) {
+      rs[i] = __shfl_sync(0xFFFFFFFFu, mine_s, i);
+      rd[i] = __shfl_sync(0xFFFFFFFFu, mine_d, i);
+    }
     evict_copy(p.k, rs, rd, p.row16, lane);
     evict_copy(p.v, rs, rd, p.row16, lane);
     evict_copy(p.sketch, rs, rd, p.sk16, lane);

@@ -10,8 +10,8 @@
 // computed in one pass with a running maximum and sum in float32, base 2.
 //
 // Here: the span and the work partition shared by the kernels, the CUDA-core
-// kernel (float32 caches, and caches in host memory) and the merge of rows
-// that several CTAs shared, which also adds the slots' attention weights.
+// kernel (float32 caches, and caches in host memory) and the join of rows that
+// several CTAs shared, which also adds the slots' attention weights.
 #pragma once
 
 #include "fasa_device.cuh"
@@ -19,6 +19,7 @@
 namespace fasa {
 
 constexpr int kSpanUnit = 64;      // slots per unit of work
+constexpr int kSpanSetup = 2;      // cost of taking up a row (queries, join), in units
 constexpr int kSpanThreads = 128;  // 4 warps
 constexpr int kSpanWarps = kSpanThreads / 32;
 constexpr int kSpanHead = 32;      // floats ahead of a partial's o: m[16], l[16]
@@ -144,34 +145,40 @@ __device__ __forceinline__ int64_t span_scan(int64_t x, int64_t* sm, int64_t& be
   return total;
 }
 
-// The units of all (b, g) rows, in that order, are dealt to n_cta CTAs in
-// equal runs: CTA c owns units [c T / n, (c + 1) T / n) of the T, n =
-// min(n_cta, T), so no run is empty. A run may begin and end inside a row;
-// such a row's CTAs leave partials.
-__device__ __forceinline__ int span_ctas(int64_t total, int n_cta) { return (int)min((int64_t)n_cta, total); }
+// The rows (b, g), in that order, cost kSpanSetup plus their units each (rows
+// without units nothing); the total T is dealt to n_cta CTAs in equal runs:
+// CTA c owns costs [c T / n, (c + 1) T / n), n = min(n_cta, T / (kSpanSetup +
+// 1)), so every run holds a unit. Unit i of a row sits at the row's first cost
+// + kSpanSetup + i. A run may begin and end inside a row; such a row's CTAs
+// leave partials. Without the setup's weight, the CTA that gets a batch's
+// short sequences takes up dozens of rows while the others stream one.
+__device__ __forceinline__ int span_ctas(int64_t total, int n_cta) {
+  return (int)min((int64_t)n_cta, total / (kSpanSetup + 1));
+}
 __device__ __forceinline__ int64_t span_cut(int64_t total, int c, int n_cta) { return total * c / n_cta; }
-// The CTA that owns unit u.
+// The CTA that owns cost u.
 __device__ __forceinline__ int span_owner(int64_t total, int64_t u, int n_cta) {
   int c = (int)((u * n_cta) / total);
   while (span_cut(total, c + 1, n_cta) <= u) ++c;
   while (span_cut(total, c, n_cta) > u) --c;
   return c;
 }
-// Totals over the sequences: the number of units, and for sequence `at` (or,
-// with at < 0, the sequence that holds unit `u`) its index and first unit.
+// A sequence's place: its index, the first cost of its KV head 0, the units
+// of one of its rows.
 struct SpanWhere {
-  int64_t total, base;  // base: first unit of sequence b (its KV head 0)
-  int b, units;         // units of one row of b
+  int64_t base;
+  int b, units;
 };
+__device__ __forceinline__ int span_cost(int units) { return units > 0 ? units + kSpanSetup : 0; }
 template <int NT>
 __device__ __forceinline__ int64_t span_total(const SpanParams& p, int64_t* sm) {
   int64_t t = 0;
-  for (int b = threadIdx.x; b < p.batch; b += NT) t += span_seq_units(p, b);
+  for (int b = threadIdx.x; b < p.batch; b += NT) t += span_cost(span_seq_units(p, b));
   int64_t before;
   return span_scan<NT>(t, sm, before) * p.n_kv_heads;
 }
-// Block-wide: finds sequence `at`, or the one that holds unit u (at < 0).
-// Returns false (b = -1) when no sequence does. `out` is shared memory.
+// Block-wide: finds sequence `at`, or the one that holds cost u (at < 0); b =
+// -1 when none does. `out` is shared memory.
 template <int NT>
 __device__ __forceinline__ void span_find(const SpanParams& p, int at, int64_t u, int64_t* sm, SpanWhere* out) {
   if (threadIdx.x == 0) out->b = -1;
@@ -180,9 +187,10 @@ __device__ __forceinline__ void span_find(const SpanParams& p, int at, int64_t u
     const int b = b0 + threadIdx.x;
     const int n = b < p.batch ? span_seq_units(p, b) : 0;
     int64_t before;
-    const int64_t sum = span_scan<NT>((int64_t)n * p.n_kv_heads, sm, before);
+    const int64_t cost = (int64_t)span_cost(n) * p.n_kv_heads;
+    const int64_t sum = span_scan<NT>(cost, sm, before);
     before += run;
-    const bool mine = at >= 0 ? b == at : (n > 0 && before <= u && u < before + (int64_t)n * p.n_kv_heads);
+    const bool mine = at >= 0 ? b == at : (n > 0 && before <= u && u < before + cost);
     if (mine) {
       out->b = b;
       out->base = before;
@@ -191,6 +199,19 @@ __device__ __forceinline__ void span_find(const SpanParams& p, int at, int64_t u
     run += sum;
   }
   __syncthreads();
+}
+
+// ------------------------------------------------------- rows seen by no one
+
+// The CTAs of a dealt grid write the zeros of sequences without units.
+template <typename T, int NT>
+__device__ __forceinline__ void span_zero_rows(const SpanParams& p) {
+  for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
+    if (span_seq_units(p, b) != 0) continue;
+    const int n = p.n_kv_heads * p.group * kD;
+    T* out = static_cast<T*>(p.out) + (int64_t)b * n;
+    for (int e = threadIdx.x; e < n; e += NT) store_f(out + e, 0.0f);
+  }
 }
 
 // --------------------------------------------------- CUDA-core attention
@@ -245,27 +266,52 @@ struct alignas(16) SpanCcSmem {
   float sc[kSpanWarps][MG];
   float m[kSpanWarps][MG], l[kSpanWarps][MG];
   float o[kSpanWarps][MG][kD];
+  double turns[kNFC];
   int64_t scan[kSpanWarps];
   SpanWhere where;
 };
 
-// The G query rows of token (b, j), KV head g, rotated at position pos and
-// scaled by log2(e) / sqrt(128), into qs [G][128] (barriers around it are the
-// caller's).
-template <typename T, int NT>
-__device__ __forceinline__ void span_queries(const SpanParams& p, int b, int j, int g, int64_t pos, float* qs) {
-  constexpr float kScale = 1.4426950408889634f * 0.08838834764831845f;
-  const int G = p.group;
-  const T* q = static_cast<const T*>(p.q) + (((int64_t)b * p.n_q + j) * p.n_kv_heads + g) * G * kD;
-  for (int e = threadIdx.x; e < G * kNFC; e += NT) {
-    const int h = e / kNFC, i = e % kNFC;
-    const float x = to_float(q[h * kD + i]), y = to_float(q[h * kD + i + kNFC]);
-    float c = 1.0f, s = 0.0f;
-    if (!p.q_prerot) span_angle(p.turns[i], pos, &c, &s);
-    qs[h * kD + i] = (x * c - y * s) * kScale;
-    qs[h * kD + i + kNFC] = (y * c + x * s) * kScale;
-  }
+// The rotation table into shared memory. Indexed per thread, the kernel
+// parameters are read one address at a time; this runs ahead of the launch
+// dependency, which the parameters do not have.
+template <int NT>
+__device__ __forceinline__ void span_stage_turns(const SpanParams& p, double* turns) {
+  for (int i = threadIdx.x; i < kNFC; i += NT) turns[i] = p.turns[i];
 }
+
+// The G query rows of token (b, j), KV head g: thread's pairs (dims i, i + 64)
+// e = tid, tid + NT, ... of the G * 64, loaded (any time ahead) and rotated at
+// position pos and scaled by log2(e) / sqrt(128) into qs [G][128].
+template <typename T, int NT, int MG>
+struct SpanQuery {
+  static constexpr int kN = (MG * kNFC + NT - 1) / NT;
+  T x[kN], y[kN];
+  __device__ __forceinline__ void load(const SpanParams& p, int b, int j, int g) {
+    const T* q = static_cast<const T*>(p.q) + (((int64_t)b * p.n_q + j) * p.n_kv_heads + g) * p.group * kD;
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+      const int e = threadIdx.x + n * NT;
+      if (e < p.group * kNFC) {
+        x[n] = q[(e / kNFC) * kD + e % kNFC];
+        y[n] = q[(e / kNFC) * kD + e % kNFC + kNFC];
+      }
+    }
+  }
+  __device__ __forceinline__ void rotate(const SpanParams& p, const double* turns, int64_t pos, float* qs) const {
+    constexpr float kScale = 1.4426950408889634f * 0.08838834764831845f;
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+      const int e = threadIdx.x + n * NT, h = e / kNFC, i = e % kNFC;
+      if (e < p.group * kNFC) {
+        const float a = to_float(x[n]), b = to_float(y[n]);
+        float c = 1.0f, s = 0.0f;
+        if (!p.q_prerot) span_angle(turns[i], pos, &c, &s);
+        qs[h * kD + i] = (a * c - b * s) * kScale;
+        qs[h * kD + i + kNFC] = (b * c + a * s) * kScale;
+      }
+    }
+  }
+};
 
 // One CTA's share of a row, units [i0, i1) of the row's n: the output when
 // that is the whole row, else partial `slot`.
@@ -277,7 +323,9 @@ __device__ __forceinline__ void span_cc_segment(const SpanParams& p, SpanCcSmem<
   const int G = p.group;
   const int64_t row = (int64_t)b * p.n_kv_heads + g;
   __syncthreads();  // the previous segment is done with shared memory
-  span_queries<T, kSpanThreads>(p, b, j, g, pos, &sm.q[0][0]);
+  SpanQuery<T, kSpanThreads, MG> raw;
+  raw.load(p, b, j, g);
+  raw.rotate(p, sm.turns, pos, &sm.q[0][0]);
   __syncthreads();
   float q[MG][4], o[MG][4];
 #pragma unroll
@@ -449,6 +497,7 @@ __device__ __forceinline__ void span_cc_segment(const SpanParams& p, SpanCcSmem<
 template <typename T, int MG>
 __global__ void __launch_bounds__(kSpanThreads) span_cc_kernel(const __grid_constant__ SpanParams p) {
   __shared__ SpanCcSmem<MG> sm;
+  span_stage_turns<kSpanThreads>(p, sm.turns);
   grid_dependency_wait();
   if (p.n_cta == 0) {
     const int b = blockIdx.y / p.n_kv_heads, g = blockIdx.y % p.n_kv_heads, j = blockIdx.x;
@@ -460,6 +509,7 @@ __global__ void __launch_bounds__(kSpanThreads) span_cc_kernel(const __grid_cons
     span_cc_segment<T, MG>(p, sm, b, j, g, v, u, pos, 0, u.n, 0);
     return;
   }
+  span_zero_rows<T, kSpanThreads>(p);
   const int64_t total = span_total<kSpanThreads>(p, sm.scan);
   const int n_cta = span_ctas(total, p.n_cta);
   if ((int)blockIdx.x >= n_cta) return;
@@ -468,9 +518,10 @@ __global__ void __launch_bounds__(kSpanThreads) span_cc_kernel(const __grid_cons
   span_find<kSpanThreads>(p, -1, u0, sm.scan, &sm.where);
   int b = sm.where.b;
   if (b < 0) return;
-  int64_t at = u0 - sm.where.base;
-  int g = (int)(at / sm.where.units), i0 = (int)(at % sm.where.units);
-  for (bool first = true; u0 < u1; first = false) {
+  const int64_t at = u0 - sm.where.base;
+  int g = (int)(at / span_cost(sm.where.units));
+  int a0 = (int)(at % span_cost(sm.where.units));  // cost within the row
+  for (bool first = true; u0 < u1;) {
     const int L = span_len(p, b);
     const int64_t pos = span_pos0(p, b, L, 1);
     const Span v = span_of(L, pos, p.window, p.n_sink);
@@ -480,10 +531,12 @@ __global__ void __launch_bounds__(kSpanThreads) span_cc_kernel(const __grid_cons
       g = 0;
       continue;
     }
-    const int i1 = (int)min((int64_t)u.n, i0 + (u1 - u0));
-    span_cc_segment<T, MG>(p, sm, b, 0, g, v, u, pos, i0, i1, 2 * blockIdx.x + (first ? 0 : 1));
-    u0 += i1 - i0;
-    i0 = 0;
+    const int a1 = (int)min((int64_t)span_cost(u.n), a0 + (u1 - u0));
+    const int i0 = max(a0 - kSpanSetup, 0), i1 = a1 - kSpanSetup;
+    if (i1 > i0) span_cc_segment<T, MG>(p, sm, b, 0, g, v, u, pos, i0, i1, 2 * blockIdx.x + (first ? 0 : 1));
+    first = false;
+    u0 += a1 - a0;
+    a0 = 0;
     if (++g == p.n_kv_heads) {
       g = 0;
       ++b;
@@ -491,62 +544,94 @@ __global__ void __launch_bounds__(kSpanThreads) span_cc_kernel(const __grid_cons
   }
 }
 
-// ------------------------------------------------------------- the merge
+// ------------------------------------------------------------- the join
 
-// Grid (rows, G + mass blocks): CTA (row, h) joins head h of a row that
-// several CTAs shared, and zeroes the outputs of a row that sees nothing; CTA
-// (row, G + x) adds the weights of the row's slots x, x + mass blocks, ... of
-// kSpanMassSlots each: mass[t] += sum_h 2^(z_ht - M_h) / L_h.
-constexpr int kSpanMassSlots = 1024;
+// The last kernel of a call. The warps of CTAs 0 .. n_mass - 1 add the
+// attention weights of their run of all rows' units (dealt like the
+// attention's, a run per warp):
+//   mass[t] += sum_h 2^(z_ht - M_h) / L_h,
+// each lane four slots, a float4 per head. The others join rows that several
+// CTAs shared, one head each: by row where there are fewer rows than CTAs
+// (by_row), else by the cuts between the runs, cut c joining the row whose
+// first unit belongs to CTA c - 1.
+struct SpanJoinParams {
+  SpanParams s;
+  int32_t n_mass;
+  int32_t by_row;
+};
+
+// The CTAs c0 .. c1 that hold a row's units and where their partials are.
+struct SpanShare {
+  int c0, c1;
+  bool opens;  // the row is the first of c0's run
+  __device__ __forceinline__ const float* part(const SpanParams& p, int c) const {
+    return p.part + (int64_t)(2 * c + (c > c0 || opens ? 0 : 1)) * (kSpanHead + p.group * kD);
+  }
+};
+__device__ __forceinline__ SpanShare span_share(const SpanParams& p, int64_t total, int64_t row_base, int units) {
+  SpanShare w;
+  const int n_cta = span_ctas(total, p.n_cta);
+  if (n_cta == 0) {  // one CTA per row
+    w.c0 = w.c1 = 0;
+    w.opens = true;
+    return w;
+  }
+  w.c0 = span_owner(total, row_base + kSpanSetup, n_cta);
+  w.c1 = span_owner(total, row_base + kSpanSetup + units - 1, n_cta);
+  w.opens = span_cut(total, w.c0, n_cta) >= row_base;
+  return w;
+}
 
 template <typename T>
-__global__ void __launch_bounds__(kSpanThreads) span_merge_kernel(const __grid_constant__ SpanParams p) {
+__global__ void __launch_bounds__(kSpanThreads) span_join_kernel(const __grid_constant__ SpanJoinParams jp) {
+  const SpanParams& p = jp.s;
   __shared__ int64_t scan[kSpanWarps];
-  __shared__ SpanWhere where;
-  __shared__ float s_m[16], s_l[16];
+  __shared__ SpanWhere where, wheres[kSpanWarps];
+  __shared__ float s_l[kSpanWarps];
   __shared__ __align__(16) float s_o[kSpanWarps][kD];
   grid_dependency_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int G = p.group, row = blockIdx.x;
-  const int b = row / p.n_kv_heads, g = row % p.n_kv_heads;
-  const bool for_out = (int)blockIdx.y < G;
+  const int G = p.group;
   const int64_t total = span_total<kSpanThreads>(p, scan);
-  span_find<kSpanThreads>(p, b, 0, scan, &where);
-  const int n = where.units;
-  T* out = static_cast<T*>(p.out) + (int64_t)row * G * kD;
-  if (n == 0) {
-    if (for_out && tid < kD) store_f(out + blockIdx.y * kD + tid, 0.0f);
-    return;
-  }
-  const int64_t ua = where.base + (int64_t)g * n, ub = ua + n;
-  const int n_cta = span_ctas(total, p.n_cta);
-  const int c0 = n_cta ? span_owner(total, ua, n_cta) : 0, c1 = n_cta ? span_owner(total, ub - 1, n_cta) : 0;
-  const int stride = kSpanHead + G * kD;
-  // partial i of the row: CTA c0's last segment unless the row opens its run,
-  // then one per CTA
-  auto part = [&](int c) {
-    const bool opens = c > c0 || span_cut(total, c, n_cta) == ua;
-    return p.part + (int64_t)(2 * c + (opens ? 0 : 1)) * stride;
-  };
-  if (for_out) {
-    if (c0 == c1) return;  // its CTA wrote the output
-    const int h = blockIdx.y;
+
+  if ((int)blockIdx.x >= jp.n_mass) {
+    const int e = blockIdx.x - jp.n_mass, h = e % G, x = e / G;
+    int64_t row, row_base;
+    if (jp.by_row) {
+      row = x;
+      span_find<kSpanThreads>(p, x / p.n_kv_heads, 0, scan, &where);
+      if (where.units == 0) return;
+      row_base = where.base + (int64_t)(x % p.n_kv_heads) * span_cost(where.units);
+    } else {
+      const int n_cta = span_ctas(total, p.n_cta), c = x + 1;
+      if (c >= n_cta) return;
+      const int64_t cut = span_cut(total, c, n_cta);
+      span_find<kSpanThreads>(p, -1, cut, scan, &where);
+      const int64_t g = (cut - where.base) / span_cost(where.units);
+      row = (int64_t)where.b * p.n_kv_heads + g;
+      row_base = where.base + g * span_cost(where.units);
+      if (cut <= row_base + kSpanSetup) return;  // the row begins behind the cut
+      if (span_owner(total, row_base + kSpanSetup, n_cta) != c - 1) return;
+    }
+    const SpanShare sh = span_share(p, total, row_base, where.units);
+    if (sh.c0 == sh.c1) return;  // its CTA wrote the output
     float M = -INFINITY;
-    for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, __ldcg(part(c) + h));
+    for (int c = sh.c0 + lane; c <= sh.c1; c += 32) M = fmaxf(M, __ldcg(sh.part(p, c) + h));
 #pragma unroll
     for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
     float L = 0.0f;
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int c = c0 + warp; c <= c1; c += kSpanWarps) {
-      const float* pp = part(c);
+#pragma unroll 4
+    for (int c = sh.c0 + warp; c <= sh.c1; c += kSpanWarps) {
+      const float* pp = sh.part(p, c);
       const float mc = __ldcg(pp + h);
       const float f = mc == -INFINITY ? 0.0f : exp2f(mc - M);
-      const float4 x = __ldcg(reinterpret_cast<const float4*>(pp + kSpanHead + h * kD) + lane);
+      const float4 x4 = __ldcg(reinterpret_cast<const float4*>(pp + kSpanHead + h * kD) + lane);
       L = __fmaf_rn(f, __ldcg(pp + 16 + h), L);
-      acc.x = __fmaf_rn(f, x.x, acc.x);
-      acc.y = __fmaf_rn(f, x.y, acc.y);
-      acc.z = __fmaf_rn(f, x.z, acc.z);
-      acc.w = __fmaf_rn(f, x.w, acc.w);
+      acc.x = __fmaf_rn(f, x4.x, acc.x);
+      acc.y = __fmaf_rn(f, x4.y, acc.y);
+      acc.z = __fmaf_rn(f, x4.z, acc.z);
+      acc.w = __fmaf_rn(f, x4.w, acc.w);
     }
     *reinterpret_cast<float4*>(&s_o[warp][lane * 4]) = acc;
     if (lane == 0) s_l[warp] = L;
@@ -558,50 +643,109 @@ __global__ void __launch_bounds__(kSpanThreads) span_merge_kernel(const __grid_c
       O += s_o[w][tid];
       L += s_l[w];
     }
-    store_f(out + h * kD + tid, L == 0.0f ? 0.0f : O / L);
+    store_f(static_cast<T*>(p.out) + (row * G + h) * kD + tid, L == 0.0f ? 0.0f : O / L);
     return;
   }
-  // the weights: every head's maximum and reciprocal sum, then the slots
-  if (c0 == c1) {
-    if (tid < G) {
-      s_m[tid] = __ldcg(p.rstat + (int64_t)row * 2 * G + tid);
-      s_l[tid] = __ldcg(p.rstat + (int64_t)row * 2 * G + G + tid);
-    }
-  } else {
-    for (int h = warp; h < G; h += kSpanWarps) {
-      float M = -INFINITY;
-      for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, __ldcg(part(c) + h));
-#pragma unroll
-      for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
-      float L = 0.0f;
-      for (int c = c0 + lane; c <= c1; c += 32) {
-        const float mc = __ldcg(part(c) + h);
-        L += mc == -INFINITY ? 0.0f : exp2f(mc - M) * __ldcg(part(c) + 16 + h);
-      }
-#pragma unroll
-      for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xFFFFFFFFu, L, o);
-      if (lane == 0) {
-        s_m[h] = M;
-        s_l[h] = L;
-      }
-    }
+
+  // the weights of this warp's run
+  const int n_run = jp.n_mass * kSpanWarps, run = blockIdx.x * kSpanWarps + warp;
+  if (total == 0) return;
+  // the sequences of the four warps' first costs, one block-wide search each
+#pragma unroll 1
+  for (int w = 0; w < kSpanWarps; ++w) {
+    const int64_t u = span_cut(total, blockIdx.x * kSpanWarps + w, n_run);
+    span_find<kSpanThreads>(p, -1, min(u, total - 1), scan, &wheres[w]);
   }
-  __syncthreads();
-  const int L = span_len(p, b);
-  const Span v = span_of(L, span_pos0(p, b, L, 1), p.window, p.n_sink);
-  const int n_blocks = gridDim.y - G;
-  for (int t0 = ((int)blockIdx.y - G) * kSpanMassSlots; t0 < v.hi; t0 += n_blocks * kSpanMassSlots) {
-    for (int t = t0 + tid; t < min(v.hi, t0 + kSpanMassSlots); t += kSpanThreads) {
-      if (!v.sees(t)) continue;
-      if (p.pm.table != nullptr &&
-          (unsigned)__ldg(p.pm.table + (int64_t)b * p.pm.max_blocks + (t >> p.pm.log2bs)) >= (unsigned)p.pm.n_pages)
-        continue;  // a skipped slot has no logit
-      float w = 0.0f;
-      for (int h = 0; h < G; ++h) {
-        const float z = __ldcg(p.logits + ((int64_t)row * G + h) * p.ld_logits + t);
-        if (s_l[h] != 0.0f) w += exp2f(z - s_m[h]) / s_l[h];
+  int64_t u0 = span_cut(total, run, n_run);
+  const int64_t u1 = span_cut(total, run + 1, n_run);
+  if (u0 >= u1) return;
+  int b = wheres[warp].b;
+  const int64_t at = u0 - wheres[warp].base;
+  const int cost0 = span_cost(wheres[warp].units);
+  int g = (int)(at / cost0), a0 = (int)(at % cost0);
+  int64_t row_base = u0 - a0;
+  const bool vec = p.mass_ld % 4 == 0 && (reinterpret_cast<uintptr_t>(p.mass) & 15) == 0;
+  while (u0 < u1) {
+    const int L = span_len(p, b);
+    const Span v = span_of(L, span_pos0(p, b, L, 1), p.window, p.n_sink);
+    const SpanUnits u = span_units(v, kSpanUnit);
+    if (u.n == 0) {
+      ++b;
+      g = 0;
+      continue;
+    }
+    const int cost = span_cost(u.n);
+    const int a1 = (int)min((int64_t)cost, a0 + (u1 - u0));
+    const int i0 = max(a0 - kSpanSetup, 0), i1 = a1 - kSpanSetup;
+    const int64_t row = (int64_t)b * p.n_kv_heads + g;
+    if (i1 > i0) {
+      // every head's maximum and reciprocal sum: lane h holds head h's
+      const SpanShare sh = span_share(p, total, row_base, u.n);
+      float m_h = -INFINITY, r_h = 0.0f;
+      if (sh.c0 == sh.c1) {
+        if (lane < G) {
+          m_h = __ldcg(p.rstat + row * 2 * G + lane);
+          r_h = __ldcg(p.rstat + row * 2 * G + G + lane);
+        }
+      } else {
+        for (int h = 0; h < G; ++h) {
+          float M = -INFINITY;
+          for (int c = sh.c0 + lane; c <= sh.c1; c += 32) M = fmaxf(M, __ldcg(sh.part(p, c) + h));
+#pragma unroll
+          for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
+          float S = 0.0f;
+          for (int c = sh.c0 + lane; c <= sh.c1; c += 32) {
+            const float mc = __ldcg(sh.part(p, c) + h);
+            S += mc == -INFINITY ? 0.0f : exp2f(mc - M) * __ldcg(sh.part(p, c) + 16 + h);
+          }
+#pragma unroll
+          for (int o = 16; o; o >>= 1) S += __shfl_xor_sync(0xFFFFFFFFu, S, o);
+          if (lane == h) {
+            m_h = M;
+            r_h = S;
+          }
+        }
       }
-      p.mass[row * p.mass_ld + t] += w;
+      r_h = r_h == 0.0f ? 0.0f : 1.0f / r_h;
+      // 16 lanes a unit, four slots each
+      for (int i = i0; i < i1; i += 2) {
+        const int iu = min(i + (lane >> 4), u.n - 1);
+        const int t = u.unit(iu) * kSpanUnit + (lane & 15) * 4;
+        bool on = i + (lane >> 4) < i1 && t < v.hi && (t + 4 > v.lo || t < v.s);
+        if (on && p.pm.table != nullptr)  // slots of a lost page have no logits
+          on = (unsigned)__ldg(p.pm.table + (int64_t)b * p.pm.max_blocks + (t >> p.pm.log2bs)) <
+               (unsigned)p.pm.n_pages;
+        const float* z = p.logits + row * G * p.ld_logits + t;
+        float w[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+        for (int h = 0; h < G; ++h) {
+          const float m = __shfl_sync(0xFFFFFFFFu, m_h, h), r = __shfl_sync(0xFFFFFFFFu, r_h, h);
+          if (on) {
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(z + h * p.ld_logits));
+            w[0] = __fmaf_rn(exp2f(x.x - m), r, w[0]);
+            w[1] = __fmaf_rn(exp2f(x.y - m), r, w[1]);
+            w[2] = __fmaf_rn(exp2f(x.z - m), r, w[2]);
+            w[3] = __fmaf_rn(exp2f(x.w - m), r, w[3]);
+          }
+        }
+        if (!on) continue;
+        float* ms = p.mass + row * p.mass_ld + t;
+        if (vec && t + 4 <= v.hi && (t >= v.lo || t + 4 <= v.s)) {
+          const float4 y = *reinterpret_cast<float4*>(ms);
+          *reinterpret_cast<float4*>(ms) = make_float4(y.x + w[0], y.y + w[1], y.z + w[2], y.w + w[3]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (v.sees(t + e)) ms[e] += w[e];
+        }
+      }
+    }
+    u0 += a1 - a0;
+    if (a1 == cost) row_base += cost;
+    a0 = 0;
+    if (++g == p.n_kv_heads) {
+      g = 0;
+      ++b;
     }
   }
 }

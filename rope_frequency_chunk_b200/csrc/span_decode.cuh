@@ -40,7 +40,7 @@ template <int GT>
 struct SdSmem {
   static constexpr int kRing = kSpanWarps * kSdStages * 2 * kSdTile;
   static constexpr int kBuf = 2 * GT * kD * 4;
-  static constexpr int kBytes = kRing + kBuf + 2 * 2 * GT * 4 + 256 + 1024;
+  static constexpr int kBytes = kRing + kBuf + 2 * 2 * GT * 4 + 256 + 512 + 1024;
 };
 
 // Row r, 16-byte chunk ch (0 .. 15) of a step's K or V: two halves of 64 dims.
@@ -55,8 +55,8 @@ __device__ __forceinline__ void sd_tma(const CUtensorMap* map, void* dst, uint64
       : "memory");
 }
 
-// Where a CTA is in its run of units: row (b, g), next unit i of the row,
-// units left in the run.
+// Where a CTA is in its run: row (b, g), next unit i of the row, costs left in
+// the run (a row's setup counts when the run takes the row up).
 struct SdCursor {
   int b, g, i;
   int64_t left;
@@ -80,6 +80,7 @@ __device__ __forceinline__ void sd_next_row(const SpanParams& p, SdCursor& c) {
     if (c.g == 0) sd_open(p, c);
   } while (c.u.n == 0);
   c.i = 0;
+  c.left -= kSpanSetup;
 }
 
 // The running softmax of a warp: for G <= 8, o[t][0..1] + o[t][2..3] are dims
@@ -232,7 +233,8 @@ __global__ void __launch_bounds__(kSpanThreads, 2) span_decode_kernel(const __gr
   float* buf = reinterpret_cast<float*>(smem + SdSmem<GT>::kRing);  // queries; two warps' o
   float* sm_m = buf + 2 * GT * kD;                                  // [2][GT]
   float* sm_l = sm_m + 2 * GT;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sm_l + 2 * GT) + warp * kSdStages;
+  double* turns = reinterpret_cast<double*>(sm_l + 2 * GT);         // [64]
+  uint64_t* full = reinterpret_cast<uint64_t*>(turns + kNFC) + warp * kSdStages;
   const int G = p.group;
 
   if (lane == 0) {
@@ -240,6 +242,7 @@ __global__ void __launch_bounds__(kSpanThreads, 2) span_decode_kernel(const __gr
     fence_mbar_init();
   }
   __syncwarp();
+  span_stage_turns<kSpanThreads>(p, turns);
   grid_dependency_wait();
 
   // the CTA's run
@@ -256,6 +259,7 @@ __global__ void __launch_bounds__(kSpanThreads, 2) span_decode_kernel(const __gr
       return;
     }
   } else {
+    span_zero_rows<__nv_bfloat16, kSpanThreads>(p);
     const int64_t total = span_total<kSpanThreads>(p, scan);
     const int n_cta = span_ctas(total, p.n_cta);
     if ((int)blockIdx.x >= n_cta) return;
@@ -263,9 +267,10 @@ __global__ void __launch_bounds__(kSpanThreads, 2) span_decode_kernel(const __gr
     span_find<kSpanThreads>(p, -1, u0, scan, &where);
     use.b = where.b;
     const int64_t at = u0 - where.base;
-    use.g = (int)(at / where.units);
-    use.i = (int)(at % where.units);
-    use.left = span_cut(total, blockIdx.x + 1, n_cta) - u0;
+    use.g = (int)(at / span_cost(where.units));
+    const int a0 = (int)(at % span_cost(where.units));
+    use.i = max(a0 - kSpanSetup, 0);
+    use.left = span_cut(total, blockIdx.x + 1, n_cta) - u0 - max(kSpanSetup - a0, 0);
     sd_open(p, use);
   }
   SdCursor get = use;  // where the loads are
@@ -275,8 +280,11 @@ __global__ void __launch_bounds__(kSpanThreads, 2) span_decode_kernel(const __gr
   // requests the warp's next step that has visible slots; false at the end
   auto request = [&]() -> bool {
     for (;;) {
-      if (get.left == 0) return false;
-      if (get.i == get.u.n) sd_next_row(p, get);
+      if (get.left <= 0) return false;
+      if (get.i == get.u.n) {
+        if (get.left <= kSpanSetup) return false;  // the run ends in the next row's setup
+        sd_next_row(p, get);
+      }
       const int t0 = get.u.unit(get.i) * kSpanUnit + warp * kSdRows;
       ++get.i;
       --get.left;
@@ -297,15 +305,26 @@ __global__ void __launch_bounds__(kSpanThreads, 2) span_decode_kernel(const __gr
     }
   };
   for (int i = 0; i < kSdStages; ++i) request();
+  SpanQuery<__nv_bfloat16, kSpanThreads, GT> next_q;  // the next row's queries, on their way
+  next_q.load(p, use.b, 0, use.g);
+  __syncthreads();  // the rotation table
 
   for (bool first = true; use.left > 0 && ok; first = false) {
-    if (use.i == use.u.n) sd_next_row(p, use);
+    if (use.i == use.u.n) {
+      if (use.left <= kSpanSetup) break;
+      sd_next_row(p, use);
+    }
     const int64_t row = (int64_t)use.b * p.n_kv_heads + use.g;
     const int i0 = use.i, i1 = (int)min((int64_t)use.u.n, i0 + use.left);
     const bool whole = i0 == 0 && i1 == use.u.n;
     for (int e = tid; e < (GT - G) * kD; e += kSpanThreads) buf[G * kD + e] = 0.0f;
-    span_queries<__nv_bfloat16, kSpanThreads>(p, use.b, 0, use.g, use.pos, buf);
+    next_q.rotate(p, turns, use.pos, buf);
     __syncthreads();
+    if (use.left - (i1 - i0) > kSpanSetup) {  // the row after this one
+      SdCursor nx = use;
+      sd_next_row(p, nx);
+      next_q.load(p, nx.b, 0, nx.g);
+    }
     SdQuery<GT> Q;
     sd_query_frags<GT>(Q, buf, lane);
     SdState<GT> st;

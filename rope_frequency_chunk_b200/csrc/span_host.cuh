@@ -264,13 +264,17 @@ fasa_status fasa_attend_decode(const fasa_cache* c, const fasa_paged* pg, const 
   }
   if ((s = launch_span_decode(c, pg, p, tc, grid, stream)) != FASA_OK) return s;
   if (p.n_cta == 0 && mass == nullptr) return FASA_OK;
-  unsigned blocks = 0;
+  SpanJoinParams jp{};
+  jp.s = p;
+  jp.by_row = rows < p.n_cta ? 1 : 0;
+  // about four CTAs per SM over the units that the rows can have
   if (mass != nullptr)
-    blocks = (unsigned)std::max<int64_t>(
-        1, std::min<int64_t>(ceil_div(sp->max_seq_len, kSpanMassSlots), ceil_div(4LL * d.sms, rows)));
-  const dim3 mgrid((unsigned)rows, (unsigned)p.group + blocks, 1);
-  return c->dtype == FASA_F32 ? launch_pdl(span_merge_kernel<float>, mgrid, kSpanThreads, 0, stream, p)
-                              : launch_pdl(span_merge_kernel<__nv_bfloat16>, mgrid, kSpanThreads, 0, stream, p);
+    jp.n_mass = (int)std::max<int64_t>(1, std::min<int64_t>(4LL * d.sms, ceil_div(rows * span_max_units(sp), 4)));
+  const int64_t joins = p.n_cta == 0 ? 0 : jp.by_row ? rows : p.n_cta - 1;
+  const dim3 jgrid((unsigned)(jp.n_mass + joins * p.group), 1, 1);
+  if (jgrid.x == 0) return FASA_OK;
+  return c->dtype == FASA_F32 ? launch_pdl(span_join_kernel<float>, jgrid, kSpanThreads, 0, stream, jp)
+                              : launch_pdl(span_join_kernel<__nv_bfloat16>, jgrid, kSpanThreads, 0, stream, jp);
 }
 
 size_t fasa_attend_prompt_workspace_bytes(const fasa_cache* c, const fasa_span* sp, int32_t n_q) {
@@ -350,6 +354,7 @@ fasa_status fasa_evict(const fasa_cache* c, const fasa_paged* pg, const fasa_evi
   if (s != FASA_OK) return s;
   if (pg != nullptr && (s = check_paged(c, pg)) != FASA_OK) return s;
   if ((s = check_evict(c, e)) != FASA_OK) return s;
+  if (span_rows(c, pg) > INT32_MAX) return FASA_ERR_UNSUPPORTED;  // rows are addressed with 32-bit indices
   if (!aligned(mass, 4) || !aligned(slot_pos, 4) || !aligned(mass_out, 4) || !aligned(slot_pos_out, 4) ||
       !aligned(len_out, 4) || len_out == e->seq_len)
     return FASA_ERR_INVALID_ARG;

@@ -222,6 +222,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) span_prompt_kernel(const __grid
     fence_mbar_init();
   }
   if (warp == 8) tc_alloc(tbase_s, 512);
+  __shared__ double turns[kNFC];
+  if (TERMS == 2) span_stage_turns<kPrThreads>(p.s, turns);
   grid_dependency_wait();
   tc_fence_before();
   __syncthreads();
@@ -238,40 +240,42 @@ __global__ void __launch_bounds__(kPrThreads, 1) span_prompt_kernel(const __grid
     unsigned char* qs = smem + sub * TERMS * kPrTile;
     const float c = 1.4426950408889634f * 0.08838834764831845f;  // log2(e) / sqrt(128)
     const __nv_bfloat16* qg = static_cast<const __nv_bfloat16*>(p.s.q);
-    // Q rows of an item into shared memory: 8 lanes per row, each the chunks
-    // ch and ch + 8 (dims i and i + 64 of 8 FCs)
+    // An item's Q rows into shared memory: 8 lanes take a token's G rows, each
+    // the chunks ch and ch + 8 (dims i and i + 64 of 8 FCs), so that an angle
+    // serves the G heads. Rows past the item's are left: what S holds there is
+    // masked.
     auto stage_q = [&](const PrItem& w) {
       const int ch = lane & 7;
-#pragma unroll 2
-      for (int s = 0; s < 8; ++s) {
-        const int rr = (warp & 3) * 32 + s * 4 + (lane >> 3);  // row of the tile
-        const int m = w.row0 + sub * 128 + rr;                 // row of the (b, g)
-        uint4 a = make_uint4(0, 0, 0, 0), b2 = a, al = a, bl = a;
-        if (sub * 128 + rr < w.n_rows) {
-          const int j = m / G, h = m % G;
-          const uint4* src = reinterpret_cast<const uint4*>(qg + (((int64_t)w.b * p.s.n_q + j) * hq + w.g * G + h) * kD);
-          a = __ldg(src + ch);
-          b2 = __ldg(src + ch + 8);
+      const int m0 = w.row0 + sub * 128, m1 = min(w.row0 + w.n_rows, m0 + 128);
+      for (int j = m0 / G + (warp & 3) * 4 + (lane >> 3); j * G < m1; j += 16) {
+        float cs[8], sn[8];
+        if (TERMS == 2) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) span_angle(turns[ch * 8 + e], w.pos0 + j, cs + e, sn + e);
+        }
+        const uint4* src = reinterpret_cast<const uint4*>(qg + (((int64_t)w.b * p.s.n_q + j) * hq + w.g * G) * kD);
+        const int h0 = max(m0 - j * G, 0), h1 = min(G, m1 - j * G);
+#pragma unroll 4
+        for (int h = h0; h < h1; ++h) {
+          const int rr = j * G + h - m0;
+          uint4 a = __ldg(src + h * 16 + ch), b2 = __ldg(src + h * 16 + ch + 8);
           if (TERMS == 2) {
             float x[8], y[8], xr[8], yr[8];
             unpack16(a, x, __nv_bfloat16());
             unpack16(b2, y, __nv_bfloat16());
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              float cs, sn;
-              span_angle(p.s.turns[ch * 8 + e], w.pos0 + j, &cs, &sn);
-              xr[e] = x[e] * cs - y[e] * sn;
-              yr[e] = y[e] * cs + x[e] * sn;
+              xr[e] = x[e] * cs[e] - y[e] * sn[e];
+              yr[e] = y[e] * cs[e] + x[e] * sn[e];
             }
+            uint4 al, bl;
             tc_split8(xr, a, al);
             tc_split8(yr, b2, bl);
+            *reinterpret_cast<uint4*>(qs + kPrTile + tc_sw(rr, ch, 128)) = al;
+            *reinterpret_cast<uint4*>(qs + kPrTile + tc_sw(rr, ch + 8, 128)) = bl;
           }
-        }
-        *reinterpret_cast<uint4*>(qs + tc_sw(rr, ch, 128)) = a;
-        *reinterpret_cast<uint4*>(qs + tc_sw(rr, ch + 8, 128)) = b2;
-        if (TERMS == 2) {
-          *reinterpret_cast<uint4*>(qs + kPrTile + tc_sw(rr, ch, 128)) = al;
-          *reinterpret_cast<uint4*>(qs + kPrTile + tc_sw(rr, ch + 8, 128)) = bl;
+          *reinterpret_cast<uint4*>(qs + tc_sw(rr, ch, 128)) = a;
+          *reinterpret_cast<uint4*>(qs + tc_sw(rr, ch + 8, 128)) = b2;
         }
       }
       fence_proxy_async_smem();
