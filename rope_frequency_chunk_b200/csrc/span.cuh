@@ -79,7 +79,7 @@ __device__ __forceinline__ SpanUnits span_units(const Span& v, int unit) {
   SpanUnits u;
   u.na = (v.s + unit - 1) / unit;
   u.first = max(v.lo / unit, u.na);
-  u.n = u.na + max(0, (v.hi + unit - 1) / unit - u.first);
+  u.n = u.na + (v.lo < v.hi ? max(0, (v.hi + unit - 1) / unit - u.first) : 0);
   return u;
 }
 

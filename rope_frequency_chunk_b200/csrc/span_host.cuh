@@ -101,10 +101,10 @@ bool span_tensor_cores(const fasa_cache* c, const fasa_paged* pg) {
   return c->dtype == FASA_BF16 && span_rows(c, pg) < INT32_MAX && !host_resident(c->k) && !host_resident(c->v);
 }
 
-// A [n_rows][128] bf16 tensor read in boxes of box_rows x 64 elements, or
-// (halves) of both 64-column halves of box_rows rows, stored for the 128-byte
-// swizzle; rows out of range read as zeros.
-fasa_status span_map(CUtensorMap* m, const void* base, int64_t n_rows, int box_rows, bool halves) {
+// A bf16 tensor read in boxes stored for the 128-byte swizzle (64 elements
+// wide); rows out of range read as zeros. strides: bytes, of dimensions 1 ..
+fasa_status span_encode(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+                        const cuuint32_t* box) {
   static std::atomic<void*> encode{nullptr};
   void* fn = encode.load(std::memory_order_acquire);
   if (fn == nullptr) {
@@ -114,14 +114,27 @@ fasa_status span_map(CUtensorMap* m, const void* base, int64_t n_rows, int box_r
       return cuda_status(e == cudaSuccess ? cudaErrorNotSupported : e);
     encode.store(fn, std::memory_order_release);
   }
-  const cuuint64_t dims[3] = {(cuuint64_t)(halves ? kD / 2 : kD), (cuuint64_t)n_rows, 2};
-  const cuuint64_t strides[2] = {kD * 2, kD};  // bytes: a row, half a row
-  const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 2}, es[3] = {1, 1, 1};
+  const cuuint32_t es[3] = {1, 1, 1};
   const CUresult r = reinterpret_cast<decltype(&cuTensorMapEncodeTiled)>(fn)(
-      m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, halves ? 3 : 2, const_cast<void*>(base), dims, strides, box, es,
+      m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, es,
       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? FASA_OK : cuda_status(cudaErrorInvalidValue);
+}
+// [n_rows][128] in boxes of box_rows x 64, or (halves) of box_rows rows' two
+// 64-column halves one behind the other.
+fasa_status span_map(CUtensorMap* m, const void* base, int64_t n_rows, int box_rows, bool halves) {
+  const cuuint64_t dims[3] = {(cuuint64_t)(halves ? kD / 2 : kD), (cuuint64_t)n_rows, 2};
+  const cuuint64_t strides[2] = {kD * 2, kD};  // a row, half a row
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 2};
+  return span_encode(m, base, halves ? 3 : 2, dims, strides, box);
+}
+// Queries [n_tokens][Hq][128] in boxes of `tokens` x G x 64.
+fasa_status span_map_q(CUtensorMap* m, const void* q, int64_t n_tokens, int hq, int group, int tokens) {
+  const cuuint64_t dims[3] = {kD, (cuuint64_t)hq, (cuuint64_t)n_tokens};
+  const cuuint64_t strides[2] = {kD * 2, (cuuint64_t)hq * kD * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)group, (cuuint32_t)tokens};
+  return span_encode(m, q, 3, dims, strides, box);
 }
 
 // Work items of a prompt call and the parts their blocks are cut into: one
@@ -135,7 +148,7 @@ struct PromptPlan {
 PromptPlan prompt_layout(const fasa_cache* c, const fasa_span* sp, int32_t n_q, int sms) {
   PromptPlan w;
   const int64_t G = c->n_q_heads / c->n_kv_heads, rows = (int64_t)c->batch * c->n_kv_heads;
-  w.tiles = ceil_div((int64_t)n_q * G, kPrRows);
+  w.tiles = ceil_div(n_q, 2 * pr_tokens((int)G));
   int64_t blocks = ceil_div(sp->max_seq_len, kPrBlock);
   if (sp->window > 0)
     blocks = std::min<int64_t>(blocks, ceil_div(sp->n_sink, kPrBlock) +
@@ -157,7 +170,7 @@ fasa_status launch_prompt_t(const PromptParams& p, int grid, cudaStream_t st) {
     return cuda_status(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
   });
   if (s != FASA_OK) return s;
-  return launch_pdl(kern, dim3((unsigned)grid, 1, 1), kPrThreads, smem, st, p);
+  return launch_pdl(kern, dim3((unsigned)grid, 1, 1), pr_threads(TERMS), smem, st, p);
 }
 
 fasa_status launch_prompt(const fasa_cache* c, const fasa_paged* pg, const fasa_span* sp, const void* q, int32_t n_q,
@@ -175,6 +188,11 @@ fasa_status launch_prompt(const fasa_cache* c, const fasa_paged* pg, const fasa_
   fasa_status s;
   if ((s = span_map(&p.map_k, c->k, p.n_rows, p.box_rows, false)) != FASA_OK) return s;
   if ((s = span_map(&p.map_v, c->v, p.n_rows, p.box_rows, false)) != FASA_OK) return s;
+  const int64_t n_tokens = (int64_t)c->batch * n_q;
+  if (n_tokens > INT32_MAX) return FASA_ERR_UNSUPPORTED;
+  if (p.s.q_prerot &&
+      (s = span_map_q(&p.map_q, q, n_tokens, c->n_q_heads, p.s.group, pr_tokens(p.s.group))) != FASA_OK)
+    return s;
   const int grid = (int)std::min<int64_t>(w.items, d.sms);
   s = p.s.q_prerot ? launch_prompt_t<1>(p, grid, st) : launch_prompt_t<2>(p, grid, st);
   if (s != FASA_OK || w.splits == 1) return s;

@@ -2,21 +2,21 @@
 // memory): Q K^T and P V with tcgen05.mma, accumulators and probabilities in
 // tensor memory, K and V blocks by TMA.
 //
-// The query rows of KV head g of a sequence are its tokens' G heads, packed:
-// row m is token m / G, head m % G, so the G heads of a token share the K and
-// V blocks they read. One work item is 256 rows (two row tiles of 128, A and
-// B) of one (b, g) over the blocks of 128 slots that any of its rows sees.
+// The query rows of KV head g of a sequence are its tokens' G heads: a row tile
+// is 128 / G whole tokens, row r token r / G, head r % G, so the G heads of a
+// token share the K and V blocks they read. One work item is two row tiles, A
+// and B, of one (b, g) over the blocks of 128 slots that any of its rows sees.
 // The CTAs (one per SM) walk the items, the longest first.
 //
-// Roles in a CTA of 12 warps (the softmax ones take registers from the rest:
-// 216 + 216 + 72 = 3 * 168):
+// Roles in a CTA (the softmax warps take registers from the others):
 //  - warps 0-3 and 4-7: the softmax of row tile A and B, one row per thread:
 //    S row from tensor memory, mask, running maximum and sum, P as bf16 into
-//    the tensor memory of S; they also stage Q and write the output;
+//    the tensor memory of S; at the end of an item its output;
 //  - warp 8: issues the products. Per block: O_A += P_A V, S_A' = Q_A K',
 //    O_B += P_B V, S_B' = Q_B K' (K' the next block): while one tile's
 //    softmax runs, the tensor core works for the other;
-//  - warp 9: K and V blocks into a ring of 32 KB stages (10 and 11: none).
+//  - warp 9: K and V blocks into a ring of 32 KB stages, and rotated queries;
+//  - warps 12-15, only where queries are rotated here: the next item's.
 // Everything one thread issues to the tensor core runs in issue order, so S_A'
 // may overwrite P_A without a wait, and S_A' done implies O_A is complete.
 //
@@ -41,14 +41,19 @@
 
 namespace fasa {
 
-constexpr int kPrThreads = 384;  // three warpgroups; 168 registers a thread at launch
-constexpr int kPrRows = 256;             // query rows per item
+constexpr int kPrRows = 256;             // query rows per item (two tiles)
+// Queries given rotated: three warpgroups, registers 200 + 200 + 104 = 3 * 168;
+// rotated here: four, 184 + 184 + 72 + 72 = 4 * 128.
+__host__ __device__ constexpr int pr_threads(int terms) { return terms == 1 ? 384 : 512; }
+// Tokens of a row tile.
+__host__ __device__ constexpr int pr_tokens(int group) { return 128 / group; }
 constexpr int kPrBlock = 128;            // slots per block
 constexpr uint32_t kPrTile = 32768;      // bytes of a 128 x 128 bf16 tile pair
 constexpr int kPrMaxSplits = 32;
 
 struct PromptParams {
   CUtensorMap map_k, map_v;  // [rows][128] bf16, boxes of box_rows x 64, 128-byte swizzle
+  CUtensorMap map_q;         // [B n_q][Hq][128], boxes of a tile's tokens x G x 64
   SpanParams s;
   int32_t n_items;           // tiles_max * B * Hkv * splits
   int32_t tiles_max;         // items of a (b, g) row at n_q queries
@@ -72,7 +77,7 @@ struct PrSmem {
 // One item as every role sees it.
 struct PrItem {
   bool valid;
-  int b, g, row0, n_rows, L, tile, split;
+  int b, g, j0, n_tok, L, tile, split;  // tokens j0 .. j0 + n_tok - 1
   int64_t pos0;      // position of the sequence's first query
   Span all;          // slots that some row of the item sees
   SpanUnits u;
@@ -97,13 +102,13 @@ __device__ __forceinline__ PrItem pr_item(const PromptParams& p, int it) {
   w.L = span_len(p.s, w.b);
   const int nq = span_qlen(p.s, w.b);
   w.pos0 = span_pos0(p.s, w.b, w.L, nq);
-  const int m_all = nq * G, tiles = (m_all + kPrRows - 1) / kPrRows;
+  const int per = 2 * pr_tokens(G), tiles = (nq + per - 1) / per;
   if (k >= tiles) return w;
   w.valid = true;
   w.tile = tiles - 1 - k;
-  w.row0 = w.tile * kPrRows;
-  w.n_rows = min(kPrRows, m_all - w.row0);
-  const int64_t pa = w.pos0 + w.row0 / G, pb = w.pos0 + (w.row0 + w.n_rows - 1) / G;
+  w.j0 = w.tile * per;
+  w.n_tok = min(per, nq - w.j0);
+  const int64_t pa = w.pos0 + w.j0, pb = pa + w.n_tok - 1;
   // the union over positions pa .. pb: the last position's end, the first
   // one's window; its sinks are slots below lo, the rest is inside anyway
   const Span first = span_of(w.L, max(pa, (int64_t)0), p.s.window, p.s.n_sink);
@@ -117,12 +122,84 @@ __device__ __forceinline__ PrItem pr_item(const PromptParams& p, int it) {
   return w;
 }
 
-__device__ __forceinline__ void pr_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// The 32-column chunks [ca, cb) of the block at slot t0 that hold slots which
+// the item sees; the products and the softmax take these alone.
+__device__ __forceinline__ void pr_chunks(const Span& all, int t0, int& ca, int& cb) {
+  const int w0 = max(all.lo, t0), w1 = min(all.hi, t0 + kPrBlock);  // the window's part
+  const int first = t0 < all.s || w1 <= w0 ? t0 : w0;
+  const int last = w1 > w0 ? w1 : min(all.s, t0 + kPrBlock);
+  ca = min((first - t0) / 32, 3);
+  cb = min(max((last - t0 + 31) / 32, ca + 1), 4);  // every listed block holds some
+}
+
+// Instruction descriptor of S = Q K^T over n columns (see tc_idesc).
+__device__ __forceinline__ uint32_t pr_idesc(int n) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
+}
+// The products, accumulating or not. One thread issues 32 of them a block, so
+// what it does per product counts: operands reach the tensor core through the
+// warp's uniform registers, so all that a batch starts from is made uniform
+// once (pr_uni) and each product adds constants to it; the accumulate
+// predicate is a constant.
+__device__ __forceinline__ uint32_t pr_uni(uint32_t x) { return __shfl_sync(0xFFFFFFFFu, x, 0); }
+__device__ __forceinline__ bool pr_elect() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
+}
+template <bool ACC>
+__device__ __forceinline__ void pr_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "n"(ACC ? 1 : 0)
+      : "memory");
+}
+template <bool ACC>
+__device__ __forceinline__ void pr_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc) {
   asm volatile(
       "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
       " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      "r"(a), "l"(b), "r"(idesc), "n"(ACC ? 1 : 0)
       : "memory");
+}
+// A descriptor (tc_desc) from its low word: start address and leading offset
+// of 16-byte units; 1024-byte stride, version, 128-byte swizzle.
+__device__ __forceinline__ uint64_t pr_desc(uint32_t lo) {
+  return ((uint64_t)((1024u >> 4) | (1u << 14) | (2u << 29)) << 32) | lo;
+}
+// S = Q K^T, TERMS terms of Q: q, k low words of the tiles' first K-step.
+template <int TERMS>
+__device__ __forceinline__ void pr_issue_s(uint32_t d, uint32_t q, uint32_t k, uint32_t idesc) {
+#pragma unroll
+  for (int t = 0; t < TERMS; ++t)
+#pragma unroll
+    for (int k8 = 0; k8 < 8; ++k8) {
+      const uint32_t o = ((k8 >> 2) * 16384 + (k8 & 3) * 32) >> 4;
+      if (t + k8 == 0)
+        pr_mma_ss<false>(d, pr_desc(q + o), pr_desc(k + o), idesc);
+      else
+        pr_mma_ss<true>(d, pr_desc(q + t * (kPrTile >> 4) + o), pr_desc(k + o), idesc);
+    }
+}
+// O (+)= P V over K-steps [2 ca, 2 cb) of 16 slots.
+template <bool FULL>
+__device__ __forceinline__ void pr_issue_o(uint32_t d, uint32_t pa, uint32_t v, int ca, int cb, bool acc) {
+  if (FULL) {
+    if (acc)
+      pr_mma_ts<true>(d, pa, pr_desc(v), tc_idesc(1));
+    else
+      pr_mma_ts<false>(d, pa, pr_desc(v), tc_idesc(1));
+#pragma unroll
+    for (int k8 = 1; k8 < 8; ++k8) pr_mma_ts<true>(d, pa + k8 * 8, pr_desc(v + k8 * (2048 >> 4)), tc_idesc(1));
+  } else {
+    for (int k8 = 2 * ca; k8 < 2 * cb; ++k8) {
+      if (acc || k8 > 2 * ca)
+        pr_mma_ts<true>(d, pa + k8 * 8, pr_desc(v + k8 * (2048 >> 4)), tc_idesc(1));
+      else
+        pr_mma_ts<false>(d, pa + k8 * 8, pr_desc(v + k8 * (2048 >> 4)), tc_idesc(1));
+    }
+  }
 }
 __device__ __forceinline__ void pr_ld32(uint32_t taddr, uint32_t* r) {
   asm volatile(
@@ -155,18 +232,75 @@ __device__ __forceinline__ void pr_st16(uint32_t taddr, const uint32_t* r) {
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-__device__ __forceinline__ void pr_st32(uint32_t taddr, const uint32_t* r) {
-  pr_st16(taddr, r);
-  pr_st16(taddr + 16, r + 16);
-}
 __device__ __forceinline__ void pr_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void pr_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
+// The larger, NaN if either is.
+__device__ __forceinline__ float pr_max(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+__device__ __forceinline__ float pr_max3(float a, float b, float c) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+// Two float32 operations in one instruction.
+__device__ __forceinline__ uint64_t pr_two(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 pr_both(uint64_t x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ uint64_t pr_fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t pr_add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// 2^x for x <= 2^20 without the special function unit, whose 16 results a
+// clock are what the softmax waits for: x = n + f with |f| <= 1/2 (n by adding
+// and subtracting 1.5 * 2^23), 2^f by a cubic fitted to the least relative
+// error with 2^0 = 1 exact (error 1.0e-4, a fortieth of P's rounding to bf16),
+// n added to the exponent. x <= -127, and -inf, give 0 exactly.
+__device__ __forceinline__ float2 pr_exp2_fma(uint64_t x2) {
+  float2 x = pr_both(x2);
+  x2 = pr_two(fmaxf(x.x, -127.0f), fmaxf(x.y, -127.0f));
+  const uint64_t big = pr_two(12582912.0f, 12582912.0f), nbig = pr_two(-12582912.0f, -12582912.0f);
+  const uint64_t t = pr_add2(x2, big);
+  const uint64_t f = pr_fma2(pr_add2(t, nbig), pr_two(-1.0f, -1.0f), x2);
+  uint64_t y = pr_fma2(f, pr_two(0.05500893294811249f, 0.05500893294811249f),
+                       pr_two(0.2422109693288803f, 0.2422109693288803f));
+  y = pr_fma2(f, y, pr_two(0.6932829022407532f, 0.6932829022407532f));
+  y = pr_fma2(f, y, pr_two(1.0f, 1.0f));
+  const float2 ti = pr_both(t), yi = pr_both(y);
+  return make_float2(__uint_as_float((__float_as_uint(ti.x) << 23) + __float_as_uint(yi.x)),
+                     __uint_as_float((__float_as_uint(ti.y) << 23) + __float_as_uint(yi.y)));
+}
+// Of every eight pairs of a row, this many take pr_exp2_fma.
+constexpr int kPrFmaPairs = 2;
+
 __device__ __forceinline__ float pr_ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+__device__ __forceinline__ void pr_tma3(const CUtensorMap* map, void* dst, uint64_t* bar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+      "[%5];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
 }
 // Tile of box_rows x 64 elements at (column x, row y) into shared memory.
 __device__ __forceinline__ void pr_tma(const CUtensorMap* map, void* dst, uint64_t* bar, int x, int y) {
@@ -190,11 +324,142 @@ __device__ __forceinline__ uint32_t pr_mask(const Span& v, int t0, int w) {
   return pr_below(v.hi - t) & (~pr_below(v.lo - t) | pr_below(v.s - t));
 }
 
+// Register k of the four lanes of a group, transposed: lane k ends up with the
+// k-th 16 bytes of each of the four lanes.
+__device__ __forceinline__ void pr_transpose4(uint32_t (&u)[16], int lane) {
+  const bool b0 = lane & 1, b1 = lane & 2;
+#pragma unroll
+  for (int i = 0; i < 4; i += 2)
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      uint32_t &lo = u[4 * i + d], &hi = u[4 * i + 4 + d];
+      const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, b0 ? lo : hi, 1);
+      if (b0) lo = got; else hi = got;
+    }
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      uint32_t &lo = u[4 * i + d], &hi = u[4 * i + 8 + d];
+      const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, b1 ? lo : hi, 2);
+      if (b1) lo = got; else hi = got;
+    }
+}
+
+// A row's state between blocks.
+struct PrRow {
+  float m_ref, l;
+  Span v;       // the slots it sees
+};
+
+// One block of a row tile: S out of tensor memory, P into it, m_ref, l and O
+// brought along. FULL: all four 32-column chunks take part, else [ca, cb).
+// bad: the block's pages outside the pool.
+template <bool FULL>
+__device__ __forceinline__ void pr_softmax(PrRow& row, uint32_t t_s, uint32_t t_o, int t0, int ca, int cb, bool first,
+                                           unsigned bad, int log2bs) {
+  constexpr float c = 1.4426950408889634f * 0.08838834764831845f;  // log2(e) / sqrt(128)
+  auto on = [&](int q) { return FULL || (q >= ca && q < cb); };
+  // S is read twice, for the maximum and for the exponentials: 32 columns at
+  // a time in registers, the next 32 on their way
+  const bool whole = t0 + kPrBlock <= row.v.hi && (t0 >= row.v.lo || t0 + kPrBlock <= row.v.s);
+  const bool masked = __any_sync(0xFFFFFFFFu, !whole) || bad;
+  uint32_t ms[4] = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};
+  if (masked) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      ms[q] = pr_mask(row.v, t0, q);
+      if (bad)
+        for (int e = 0; e < 32; ++e)
+          if ((bad >> min((q * 32 + e) >> log2bs, 31)) & 1u) ms[q] &= ~(1u << e);
+    }
+  }
+  auto hide = [&](uint32_t* s, int q) {
+    if (masked) {
+#pragma unroll
+      for (int e = 0; e < 32; ++e)
+        if (!((ms[q] >> e) & 1u)) s[e] = 0xFF800000u;  // -inf
+    }
+  };
+  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+  uint32_t sa[32], sb[32];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if (on(2 * h)) pr_ld32(t_s + 64 * h, sa);
+    if (on(2 * h + 1)) pr_ld32(t_s + 64 * h + 32, sb);
+    auto top = [&](uint32_t* s, int q) {
+      if (!on(q)) return;
+      pr_ld_wait(s);
+      hide(s, q);
+#pragma unroll
+      for (int e = 0; e < 32; e += 2)
+        mx[(e >> 1) & 3] = pr_max3(mx[(e >> 1) & 3], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+    };
+    top(sa, 2 * h);
+    top(sb, 2 * h + 1);
+  }
+  if (on(0)) pr_ld32(t_s, sa);
+  const float m_blk = pr_max(pr_max(mx[0], mx[1]), pr_max(mx[2], mx[3])) * c;
+  if (m_blk != m_blk) row.l = m_blk;  // a NaN logit
+  const bool grow = m_blk > row.m_ref + 8.0f || (row.m_ref == -INFINITY && m_blk > -INFINITY);
+  if (__any_sync(0xFFFFFFFFu, grow)) {
+    const float m_new = grow ? m_blk : row.m_ref;
+    const float f = row.m_ref == -INFINITY ? 0.0f : pr_ex2(row.m_ref - m_new);
+    if (!first && __any_sync(0xFFFFFFFFu, grow && row.m_ref > -INFINITY)) {
+      const float fo = grow ? f : 1.0f;
+#pragma unroll 1
+      for (int q = 0; q < 4; ++q) {
+        pr_ld32(t_o + q * 32, sb);
+        pr_ld_wait(sb);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) sb[e] = __float_as_uint(__uint_as_float(sb[e]) * fo);
+        pr_st16(t_o + q * 32, sb);
+        pr_st16(t_o + q * 32 + 16, sb + 16);
+      }
+    }
+    if (grow) {
+      row.l *= f;
+      row.m_ref = m_new;
+    }
+  }
+  const float off = row.m_ref == -INFINITY ? 0.0f : -row.m_ref;
+  const uint64_t c2 = pr_two(c, c), off2 = pr_two(off, off);
+  uint64_t ls[2] = {0, 0};
+  auto probs = [&](uint32_t* s, uint32_t* ahead, int q) {
+    if (on(q)) pr_ld_wait(s);
+    if (q < 3 && on(q + 1)) pr_ld32(t_s + (q + 1) * 32, ahead);
+    if (!on(q)) return;
+    hide(s, q);
+    uint32_t pk[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const uint64_t x = pr_fma2(pr_two(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), c2, off2);
+      float2 y;
+      if ((e & 7) < kPrFmaPairs) {
+        y = pr_exp2_fma(x);
+      } else {
+        y = pr_both(x);
+        y = make_float2(pr_ex2(y.x), pr_ex2(y.y));
+      }
+      ls[e & 1] = pr_add2(ls[e & 1], pr_two(y.x, y.y));
+      pk[e] = tc_pack(y.x, y.y);
+    }
+    pr_st16(t_s + q * 16, pk);
+  };
+  probs(sa, sb, 0);
+  probs(sb, sa, 1);
+  probs(sa, sb, 2);
+  probs(sb, sa, 3);
+  const float2 a = pr_both(pr_add2(ls[0], ls[1]));
+  row.l += a.x + a.y;
+}
+
 template <int TERMS>
-__global__ void __launch_bounds__(kPrThreads, 1) span_prompt_kernel(const __grid_constant__ PromptParams p) {
+__global__ void __launch_bounds__(pr_threads(TERMS), 1) span_prompt_kernel(const __grid_constant__ PromptParams p) {
   using SM = PrSmem<TERMS>;
   constexpr int kStages = SM::kStages;
   extern __shared__ __align__(16) unsigned char smem_raw[];
+  __shared__ double turns[kNFC];
   const uint32_t raw = smem_u32(smem_raw);
   unsigned char* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
   unsigned char* ring = smem + SM::kQ;
@@ -204,9 +469,10 @@ __global__ void __launch_bounds__(kPrThreads, 1) span_prompt_kernel(const __grid
   uint64_t* bar_p = bar_s + 2;        // [2] P is in tensor memory
   uint64_t* bar_o = bar_p + 2;        // [2] an item's O is complete
   uint64_t* bar_q = bar_o + 2;        // [2] an item's Q is staged
-  uint32_t* tbase_s = reinterpret_cast<uint32_t*>(bar_q + 2);
+  uint64_t* bar_f = bar_q + 2;        // [2] an item's Q is no longer read
+  uint32_t* tbase_s = reinterpret_cast<uint32_t*>(bar_f + 2);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int G = p.s.group, hq = p.s.n_kv_heads * G;
+  const int G = p.s.group, hq = p.s.n_kv_heads * G, tt = pr_tokens(G);
 
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -217,13 +483,13 @@ __global__ void __launch_bounds__(kPrThreads, 1) span_prompt_kernel(const __grid
       mbar_init(bar_s + i, 1);
       mbar_init(bar_p + i, 128);
       mbar_init(bar_o + i, 1);
-      mbar_init(bar_q + i, 128);
+      mbar_init(bar_q + i, TERMS == 1 ? 1 : 128);
+      mbar_init(bar_f + i, 1);
     }
     fence_mbar_init();
   }
   if (warp == 8) tc_alloc(tbase_s, 512);
-  __shared__ double turns[kNFC];
-  if (TERMS == 2) span_stage_turns<kPrThreads>(p.s, turns);
+  if (TERMS == 2) span_stage_turns<pr_threads(TERMS)>(p.s, turns);
   grid_dependency_wait();
   tc_fence_before();
   __syncthreads();
@@ -233,184 +499,83 @@ __global__ void __launch_bounds__(kPrThreads, 1) span_prompt_kernel(const __grid
 
   if (warp < 8) {
     // ------------------------------------------------ softmax of one tile
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    if (TERMS == 1)
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    else
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
     const int sub = warp >> 2, r = tid & 127;  // row of the tile = TMEM lane
+    const int rt = r / G, rh = r % G;          // its token and head
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t t_s = tbase + sub * 128 + lanes, t_o = tbase + 256 + sub * 128 + lanes;
-    unsigned char* qs = smem + sub * TERMS * kPrTile;
-    const float c = 1.4426950408889634f * 0.08838834764831845f;  // log2(e) / sqrt(128)
-    const __nv_bfloat16* qg = static_cast<const __nv_bfloat16*>(p.s.q);
-    // An item's Q rows into shared memory: 8 lanes take a token's G rows, each
-    // the chunks ch and ch + 8 (dims i and i + 64 of 8 FCs), so that an angle
-    // serves the G heads. Rows past the item's are left: what S holds there is
-    // masked.
-    auto stage_q = [&](const PrItem& w) {
-      const int ch = lane & 7;
-      const int m0 = w.row0 + sub * 128, m1 = min(w.row0 + w.n_rows, m0 + 128);
-      for (int j = m0 / G + (warp & 3) * 4 + (lane >> 3); j * G < m1; j += 16) {
-        float cs[8], sn[8];
-        if (TERMS == 2) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) span_angle(turns[ch * 8 + e], w.pos0 + j, cs + e, sn + e);
-        }
-        const uint4* src = reinterpret_cast<const uint4*>(qg + (((int64_t)w.b * p.s.n_q + j) * hq + w.g * G) * kD);
-        const int h0 = max(m0 - j * G, 0), h1 = min(G, m1 - j * G);
-#pragma unroll 4
-        for (int h = h0; h < h1; ++h) {
-          const int rr = j * G + h - m0;
-          uint4 a = __ldg(src + h * 16 + ch), b2 = __ldg(src + h * 16 + ch + 8);
-          if (TERMS == 2) {
-            float x[8], y[8], xr[8], yr[8];
-            unpack16(a, x, __nv_bfloat16());
-            unpack16(b2, y, __nv_bfloat16());
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              xr[e] = x[e] * cs[e] - y[e] * sn[e];
-              yr[e] = y[e] * cs[e] + x[e] * sn[e];
-            }
-            uint4 al, bl;
-            tc_split8(xr, a, al);
-            tc_split8(yr, b2, bl);
-            *reinterpret_cast<uint4*>(qs + kPrTile + tc_sw(rr, ch, 128)) = al;
-            *reinterpret_cast<uint4*>(qs + kPrTile + tc_sw(rr, ch + 8, 128)) = bl;
-          }
-          *reinterpret_cast<uint4*>(qs + tc_sw(rr, ch, 128)) = a;
-          *reinterpret_cast<uint4*>(qs + tc_sw(rr, ch + 8, 128)) = b2;
-        }
-      }
-      fence_proxy_async_smem();
-      pr_arrive(bar_q + sub);
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.s.out);
+    auto part_of = [&](const PrItem& w) {
+      return p.part + (((int64_t)(w.b * p.s.n_kv_heads + w.g) * p.tiles_max + w.tile) * p.splits + w.split) * kPrPart;
     };
-    // the next item with blocks and rows for this tile, from `it` on; items
-    // without blocks get their zeros on the way
-    uint32_t n_s = 0, n_o = 0;  // barrier phases used
+    auto has_row = [&](const PrItem& w) { return rt < tt && sub * tt + rt < w.n_tok; };
+    auto out_row = [&](const PrItem& w) {  // row of out [B n_q Hq][128]
+      return ((int64_t)w.b * p.s.n_q + w.j0 + sub * tt + rt) * hq + w.g * G + rh;
+    };
+    // the next item with blocks, from `it` on; items without get their zeros
+    // on the way
     auto next = [&](int& it, PrItem& w) -> bool {
       for (;; ++it) {
         w = pr_item(p, it);
         if (w.b < 0) return false;
         if (!w.valid) continue;
-        const bool mine = sub * 128 + r < w.n_rows;
         if (w.i0 < w.i1) return true;
+        if (!has_row(w)) continue;
         if (p.splits > 1) {
-          if (mine) {
-            float* pp = p.part + (((int64_t)(w.b * p.s.n_kv_heads + w.g) * p.tiles_max + w.tile) * p.splits + w.split) *
-                                     kPrPart;
-            pp[sub * 128 + r] = -INFINITY;
-            pp[kPrRows + sub * 128 + r] = 0.0f;
-          }
-        } else if (mine) {
-          const int m = w.row0 + sub * 128 + r;
-          uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.s.out) +
-                                              (((int64_t)w.b * p.s.n_q + m / G) * hq + w.g * G + m % G) * kD);
+          float* pp = part_of(w);
+          pp[sub * 128 + r] = -INFINITY;
+          pp[kPrRows + sub * 128 + r] = 0.0f;
+        } else {
+          uint4* o = reinterpret_cast<uint4*>(out + out_row(w) * kD);
 #pragma unroll
           for (int i = 0; i < 16; ++i) o[i] = make_uint4(0, 0, 0, 0);
         }
       }
     };
+    uint32_t n_s = 0, n_o = 0;  // barrier phases used
     int it = 0;
     PrItem w;
     bool more = next(it, w), ok = true;
-    // a tile B without rows takes no part in its item
-    if (more && sub * 128 < w.n_rows) stage_q(w);
+    const int n_pg = p.s.pm.table ? max(1, kPrBlock >> p.s.pm.log2bs) : 0;
     while (more && ok) {
-      const bool active = sub * 128 < w.n_rows;
-      float m_ref = -INFINITY, l = 0.0f;
-      const int m = w.row0 + sub * 128 + r;
-      const bool mine = sub * 128 + r < w.n_rows;
-      const Span v = span_of(w.L, mine ? w.pos0 + m / G : -1, p.s.window, p.s.n_sink);
-      if (active) {
-        // bad pages of the next block: bit i for its i-th page
-        const int n_pg = p.s.pm.table ? max(1, kPrBlock >> p.s.pm.log2bs) : 0;
-        auto bad_pages = [&](int i) -> unsigned {
-          if (n_pg == 0 || i >= w.i1) return 0u;
-          const int t = w.u.unit(i) * kPrBlock + (lane << p.s.pm.log2bs);
-          bool bad = false;
-          if (lane < n_pg && t < w.all.hi)
-            bad = (unsigned)__ldg(p.s.pm.table + (int64_t)w.b * p.s.pm.max_blocks + (t >> p.s.pm.log2bs)) >=
-                  (unsigned)p.s.pm.n_pages;
-          return __ballot_sync(0xFFFFFFFFu, bad);
-        };
+      const bool mine = has_row(w);
+      if (sub * tt < w.n_tok) {
+        PrRow row;
+        row.m_ref = -INFINITY;
+        row.l = 0.0f;
+        row.v = span_of(w.L, mine ? w.pos0 + w.j0 + sub * tt + rt : -1, p.s.window, p.s.n_sink);
         for (int i = w.i0; i < w.i1; ++i) {
           const int t0 = w.u.unit(i) * kPrBlock;
-          const unsigned bad = bad_pages(i);
+          unsigned bad = 0;  // the block's pages outside the pool
+          if (n_pg) {
+            const int t = t0 + (lane << p.s.pm.log2bs);
+            bad = __ballot_sync(0xFFFFFFFFu,
+                                lane < n_pg && t < w.all.hi &&
+                                    (unsigned)__ldg(p.s.pm.table + (int64_t)w.b * p.s.pm.max_blocks +
+                                                    (t >> p.s.pm.log2bs)) >= (unsigned)p.s.pm.n_pages);
+          }
+          int ca, cb;
+          pr_chunks(w.all, t0, ca, cb);
           if (!pr_wait(bar_s + sub, n_s & 1)) {
             ok = false;
             break;
           }
           ++n_s;
           tc_fence_after();
-          uint32_t s[128];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) pr_ld32(t_s + q * 32, s + q * 32);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) pr_ld_wait(s + q * 32);
-          const bool whole = t0 + kPrBlock <= v.hi && (t0 >= v.lo || t0 + kPrBlock <= v.s);
-          if (__any_sync(0xFFFFFFFFu, !whole) || bad) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              uint32_t ms = pr_mask(v, t0, q);
-              if (bad) {
-                for (int e = 0; e < 32; ++e)
-                  if ((bad >> min((q * 32 + e) >> p.s.pm.log2bs, 31)) & 1u) ms &= ~(1u << e);
-              }
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (!((ms >> e) & 1u)) s[q * 32 + e] = 0xFF800000u;  // -inf
-            }
-          }
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int e = 0; e < 128; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(s[e]));
-          const float m_blk = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-          const bool grow = m_blk > m_ref + 8.0f || (m_ref == -INFINITY && m_blk > -INFINITY);
-          if (__any_sync(0xFFFFFFFFu, grow)) {
-            const float m_new = grow ? m_blk : m_ref;
-            const float f = m_ref == -INFINITY ? 0.0f : pr_ex2(m_ref - m_new);
-            if (i > w.i0 && __any_sync(0xFFFFFFFFu, grow && m_ref > -INFINITY)) {
-              const float fo = grow ? f : 1.0f;
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                uint32_t o[32];
-                pr_ld32(t_o + q * 32, o);
-                pr_ld_wait(o);
-#pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fo);
-                pr_st32(t_o + q * 32, o);
-              }
-            }
-            if (grow) {
-              l *= f;
-              m_ref = m_new;
-            }
-          }
-          const float off = m_ref == -INFINITY ? 0.0f : m_ref;
-          float ls[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const float a = pr_ex2(__fmaf_rn(__uint_as_float(s[q * 32 + e]), c, -off));
-              const float b2 = pr_ex2(__fmaf_rn(__uint_as_float(s[q * 32 + e + 1]), c, -off));
-              ls[(e >> 1) & 1] += a;
-              ls[2 + ((e >> 1) & 1)] += b2;
-              pk[e >> 1] = tc_pack(a, b2);
-            }
-            pr_st16(t_s + q * 16, pk);
-          }
-          l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+          if (cb - ca == 4)
+            pr_softmax<true>(row, t_s, t_o, t0, 0, 4, i == w.i0, bad, p.s.pm.log2bs);
+          else
+            pr_softmax<false>(row, t_s, t_o, t0, ca, cb, i == w.i0, bad, p.s.pm.log2bs);
           pr_st_wait();
           tc_fence_before();
           pr_arrive(bar_p + sub);
         }
-      }
-      if (!ok) break;
-      // the next item's queries go in while this one's last product runs
-      const PrItem done = w;
-      ++it;
-      more = next(it, w);
-      if (more && sub * 128 < w.n_rows) stage_q(w);
-      if (active) {
+        if (!ok) break;
+        const int64_t at = mine ? out_row(w) : -1;
+        float* pp = p.splits > 1 ? part_of(w) : nullptr;
         if (!pr_wait(bar_o + sub, n_o & 1)) {
           ok = false;
           break;
@@ -418,34 +583,34 @@ __global__ void __launch_bounds__(kPrThreads, 1) span_prompt_kernel(const __grid
         ++n_o;
         tc_fence_after();
         if (p.splits == 1) {
-          const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-          uint4* og = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.s.out) +
-                                               (((int64_t)done.b * p.s.n_q + m / G) * hq + done.g * G + m % G) * kD);
+          // rows of the lane's group of four: lane k stores the k-th 16 bytes
+          // of each 64, so that a group's store covers 64 bytes of a row
+          int64_t at4[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) at4[k] = __shfl_sync(0xFFFFFFFFu, at, (lane & ~3) + k);
+          const float inv = row.l == 0.0f ? 0.0f : 1.0f / row.l;
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            uint32_t o[32];
+            uint32_t o[32], z[16];
             pr_ld32(t_o + q * 32, o);
             pr_ld_wait(o);
-            if (mine) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                uint32_t z[4];
-#pragma unroll
-                for (int d = 0; d < 4; ++d) {
-                  const float x0 = __uint_as_float(o[e * 8 + 2 * d]) * inv, x1 = __uint_as_float(o[e * 8 + 2 * d + 1]) * inv;
-                  z[d] = l == 0.0f ? 0u : tc_pack(x0, x1);
-                }
-                og[q * 4 + e] = make_uint4(z[0], z[1], z[2], z[3]);
-              }
+            for (int d = 0; d < 16; ++d) {
+              const float x0 = __uint_as_float(o[2 * d]) * inv, x1 = __uint_as_float(o[2 * d + 1]) * inv;
+              z[d] = row.l == 0.0f ? 0u : tc_pack(x0, x1);
             }
+            pr_transpose4(z, lane);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (at4[k] >= 0)
+                reinterpret_cast<uint4*>(out + at4[k] * kD)[q * 4 + (lane & 3)] =
+                    make_uint4(z[4 * k], z[4 * k + 1], z[4 * k + 2], z[4 * k + 3]);
           }
         } else {
-          float* pp = p.part + (((int64_t)(done.b * p.s.n_kv_heads + done.g) * p.tiles_max + done.tile) * p.splits +
-                                done.split) * kPrPart;
           const int rr = sub * 128 + r;
           if (mine) {
-            pp[rr] = m_ref;
-            pp[kPrRows + rr] = l;
+            pp[rr] = row.m_ref;
+            pp[kPrRows + rr] = row.l;
           }
           uint4* po = reinterpret_cast<uint4*>(pp + 2 * kPrRows + (int64_t)rr * kD);
 #pragma unroll
@@ -461,7 +626,11 @@ __global__ void __launch_bounds__(kPrThreads, 1) span_prompt_kernel(const __grid
         }
         tc_fence_before();
       }
+      ++it;
+      more = next(it, w);
     }
+  } else if (TERMS == 1) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
   }
@@ -469,32 +638,37 @@ __global__ void __launch_bounds__(kPrThreads, 1) span_prompt_kernel(const __grid
     // ----------------------------------------------------- the products
     uint32_t kv = 0, n_p[2] = {0, 0}, n_q[2] = {0, 0};
     bool ok = true;
-    const uint32_t q_addr = smem_u32(smem), r_addr = smem_u32(ring);
+    // low descriptor words of Q of tile A, of a block as K (rows of chunk 0),
+    // as V (64-dim halves 16 KB apart)
+    const uint32_t tb = pr_uni(tbase);
+    const uint32_t q_lo = pr_uni((smem_u32(smem) >> 4) | (1u << 16)), k_lo = pr_uni((smem_u32(ring) >> 4) | (1u << 16)),
+                   v_lo = pr_uni((smem_u32(ring) >> 4) | ((16384u >> 4) << 16));
     auto wait_full = [&](uint32_t n) { return pr_wait(full + n % kStages, (n / kStages) & 1); };
-    // S of tile `sub` = its queries times the block in stage `st`
-    auto issue_s = [&](int sub, uint32_t st) {
-      const uint32_t ks = r_addr + st * kPrTile, qa = q_addr + sub * TERMS * kPrTile;
-#pragma unroll
-      for (int t = 0; t < TERMS; ++t)
-#pragma unroll
-        for (int k8 = 0; k8 < 8; ++k8) {
-          const uint32_t o = (k8 >> 2) * 16384 + (k8 & 3) * 32;
-          tc_mma(tbase + sub * 128, tc_desc(qa + t * kPrTile + o, 16, 1024), tc_desc(ks + o, 16, 1024), tc_idesc(0),
-                 t + k8 > 0);
-        }
-      tc_commit(bar_s + sub);
+    // S of tile `sub` = its queries times chunks [ca, cb) of the block in
+    // stage `st`; after an item's last one its queries are free
+    auto issue_s = [&](int sub, uint32_t st, int ca, int cb, bool last, bool release) {
+      const uint32_t d = pr_uni(tb + sub * 128 + ca * 32), q = pr_uni(q_lo + sub * (TERMS * kPrTile >> 4)),
+                     k = pr_uni(k_lo + st * (kPrTile >> 4) + ca * (4096 >> 4)), id = pr_uni(pr_idesc(32 * (cb - ca)));
+      if (pr_elect()) {
+        pr_issue_s<TERMS>(d, q, k, id);
+        tc_commit(bar_s + sub);
+        if (last) tc_commit(bar_f + sub);
+        if (release) tc_commit(empty + st);
+      }
+      __syncwarp();
     };
     for (int it = 0; ok; ++it) {
       const PrItem w = pr_item(p, it);
       if (w.b < 0) break;
       if (!w.valid || w.i0 >= w.i1) continue;
-      const int subs = w.n_rows > 128 ? 2 : 1;
-      for (int sub = 0; sub < subs && ok; ++sub) ok = pr_wait(bar_q + sub, n_q[sub]++ & 1);
-      if (!ok || !(ok = wait_full(kv))) break;
-      tc_fence_after();
-      if (lane == 0) {
-        for (int sub = 0; sub < subs; ++sub) issue_s(sub, kv % kStages);
-        tc_commit(empty + kv % kStages);
+      const int subs = w.n_tok > tt ? 2 : 1;
+      int ca, cb;
+      pr_chunks(w.all, w.u.unit(w.i0) * kPrBlock, ca, cb);
+      if (!(ok = wait_full(kv))) break;
+      for (int sub = 0; sub < subs && ok; ++sub) {
+        if (!(ok = pr_wait(bar_q + sub, n_q[sub]++ & 1))) break;
+        tc_fence_after();
+        issue_s(sub, kv % kStages, ca, cb, w.i1 - w.i0 == 1, sub == subs - 1);
       }
       ++kv;
       for (int i = w.i0; i < w.i1 && ok; ++i) {
@@ -504,47 +678,51 @@ __global__ void __launch_bounds__(kPrThreads, 1) span_prompt_kernel(const __grid
         if (!last) ++kv;
         if (!(ok = wait_full(v_n))) break;
         const uint32_t vs_st = v_n % kStages;
-        // rows of the block that nobody sees: zeros
+        // rows of the block's chunks that nobody sees: zeros
         const int t0 = w.u.unit(i) * kPrBlock;
         if (t0 + kPrBlock > w.all.hi || (t0 < w.all.lo && t0 + kPrBlock > w.all.s)) {
           unsigned char* vs = ring + vs_st * kPrTile;
           auto zero = [&](int ra, int rb) {  // rows ra .. rb - 1
-            for (int e = max(ra, 0) * 8 + lane; e < min(rb, kPrBlock) * 8; e += 32) {
+            for (int e = ra * 8 + lane; e < rb * 8; e += 32) {
               *reinterpret_cast<uint4*>(vs + e * 16) = make_uint4(0, 0, 0, 0);
               *reinterpret_cast<uint4*>(vs + 16384 + e * 16) = make_uint4(0, 0, 0, 0);
             }
           };
-          zero(w.all.s - t0, w.all.lo - t0);
-          zero(w.all.hi - t0, kPrBlock);
+          zero(max(w.all.s - t0, ca * 32), min(w.all.lo - t0, cb * 32));
+          zero(max(w.all.hi - t0, ca * 32), cb * 32);
           fence_proxy_async_smem();
           __syncwarp();
         }
+        int na = 0, nb = 1;  // the next block's chunks
+        if (!last) pr_chunks(w.all, w.u.unit(i + 1) * kPrBlock, na, nb);
         for (int sub = 0; sub < subs && ok; ++sub) {
           if (!(ok = pr_wait(bar_p + sub, n_p[sub]++ & 1))) break;
           tc_fence_after();
-          if (lane == 0) {
-            const uint32_t vs = r_addr + vs_st * kPrTile;
-#pragma unroll
-            for (int k8 = 0; k8 < 8; ++k8)
-              pr_mma_ts(tbase + 256 + sub * 128, tbase + sub * 128 + k8 * 8, tc_desc(vs + k8 * 2048, 16384, 1024),
-                        tc_idesc(1), i > w.i0 || k8 > 0);
-            if (last) tc_commit(bar_o + sub);
-            if (sub == subs - 1) tc_commit(empty + vs_st);
+          {
+            const uint32_t d = pr_uni(tb + 256 + sub * 128), pa = pr_uni(tb + sub * 128),
+                           v = pr_uni(v_lo + vs_st * (kPrTile >> 4));
+            if (pr_elect()) {
+              if (cb - ca == 4)
+                pr_issue_o<true>(d, pa, v, 0, 4, i > w.i0);
+              else
+                pr_issue_o<false>(d, pa, v, ca, cb, i > w.i0);
+              if (last) tc_commit(bar_o + sub);
+              if (sub == subs - 1) tc_commit(empty + vs_st);
+            }
+            __syncwarp();
           }
           if (!last) {
             if (sub == 0 && !(ok = wait_full(k_n))) break;
-            if (lane == 0) {
-              issue_s(sub, k_n % kStages);
-              if (sub == subs - 1) tc_commit(empty + k_n % kStages);
-            }
+            issue_s(sub, k_n % kStages, na, nb, i + 2 == w.i1, sub == subs - 1);
           }
-          __syncwarp();
         }
+        ca = na;
+        cb = nb;
       }
     }
   } else if (warp == 9) {
     // ------------------------------------------------------- the loads
-    uint32_t n = 0;
+    uint32_t n = 0, n_f[2] = {0, 0};
     bool ok = true;
     const int boxes = kPrBlock / p.box_rows;
     auto load = [&](const PrItem& w, int i, bool is_v) {
@@ -579,12 +757,80 @@ __global__ void __launch_bounds__(kPrThreads, 1) span_prompt_kernel(const __grid
       for (int i = w.i0; i < w.i1 && ok; ++i) {
         load(w, i, false);
         if (ok) load(w, i, true);
+        if (TERMS == 1 && i == w.i0) {  // behind the first block, which does not wait for the queries' place
+          for (int sub = 0; sub < 2 && ok && sub * tt < w.n_tok; ++sub) {
+            if (n_f[sub] > 0 && !pr_wait(bar_f + sub, (n_f[sub] - 1) & 1)) {
+              ok = false;
+              break;
+            }
+            ++n_f[sub];
+            if (lane == 0) {
+              mbar_arrive_expect_tx(bar_q + sub, (uint32_t)(tt * G) * 256u);
+              for (int half = 0; half < 2; ++half)
+                pr_tma3(&p.map_q, smem + sub * kPrTile + half * 16384, bar_q + sub, half * 64, w.g * G,
+                        w.b * p.s.n_q + w.j0 + sub * tt);
+            }
+            __syncwarp();
+          }
+        }
       }
     }
     // every copy has landed before the block ends (the products wait for
     // them all unless something went wrong)
     for (uint32_t k = n > (uint32_t)kStages ? n - kStages : 0; k < n; ++k)
       mbar_wait(full + k % kStages, (k / kStages) & 1);
+    if (TERMS == 1)
+      for (int sub = 0; sub < 2; ++sub)
+        if (n_f[sub] > 0) mbar_wait(bar_q + sub, (n_f[sub] - 1) & 1);
+  } else if (TERMS == 2 && warp >= 12) {
+    // ---------------------------------------------- rotated queries, two terms
+    uint32_t n_f[2] = {0, 0};
+    bool ok = true;
+    const __nv_bfloat16* qg = static_cast<const __nv_bfloat16*>(p.s.q);
+    const int ch = lane & 7;  // 8 lanes a token, each the chunks ch and ch + 8 (dims i and i + 64 of 8 FCs)
+    for (int it = 0; ok; ++it) {
+      const PrItem w = pr_item(p, it);
+      if (w.b < 0) break;
+      if (!w.valid || w.i0 >= w.i1) continue;
+      for (int sub = 0; sub < 2 && sub * tt < w.n_tok; ++sub) {
+        unsigned char* qs = smem + sub * TERMS * kPrTile;
+        const int jt0 = (warp & 3) * 4 + (lane >> 3), n_t = min(tt, w.n_tok - sub * tt);
+        const __nv_bfloat16* base = qg + (((int64_t)w.b * p.s.n_q + w.j0 + sub * tt) * hq + w.g * G) * kD;
+        for (int e = (warp & 3) * 32 + lane; e < n_t * 2 * G; e += 128)  // on their way to L2 meanwhile
+          prefetch_line_l2(base + (int64_t)(e / (2 * G)) * hq * kD + (e % (2 * G)) * 64);
+        if (n_f[sub] > 0 && !pr_wait(bar_f + sub, (n_f[sub] - 1) & 1)) {
+          ok = false;
+          break;
+        }
+        ++n_f[sub];
+        for (int jt = jt0; jt < n_t; jt += 16) {
+          float cs[8], sn[8];  // an angle serves the G heads
+#pragma unroll
+          for (int e = 0; e < 8; ++e) span_angle(turns[ch * 8 + e], w.pos0 + w.j0 + sub * tt + jt, cs + e, sn + e);
+          const uint4* src = reinterpret_cast<const uint4*>(base + (int64_t)jt * hq * kD);
+#pragma unroll 2
+          for (int h = 0; h < G; ++h) {
+            const int rr = jt * G + h;
+            float x[8], y[8], t8[8];
+            unpack16(__ldg(src + h * 16 + ch), x, __nv_bfloat16());
+            unpack16(__ldg(src + h * 16 + ch + 8), y, __nv_bfloat16());
+            uint4 hi, lo;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) t8[e] = x[e] * cs[e] - y[e] * sn[e];
+            tc_split8(t8, hi, lo);
+            *reinterpret_cast<uint4*>(qs + tc_sw(rr, ch, 128)) = hi;
+            *reinterpret_cast<uint4*>(qs + kPrTile + tc_sw(rr, ch, 128)) = lo;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) t8[e] = y[e] * cs[e] + x[e] * sn[e];
+            tc_split8(t8, hi, lo);
+            *reinterpret_cast<uint4*>(qs + tc_sw(rr, ch + 8, 128)) = hi;
+            *reinterpret_cast<uint4*>(qs + kPrTile + tc_sw(rr, ch + 8, 128)) = lo;
+          }
+        }
+        fence_proxy_async_smem();
+        pr_arrive(bar_q + sub);
+      }
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -597,12 +843,12 @@ __global__ void __launch_bounds__(128) span_prompt_merge_kernel(const __grid_con
   grid_dependency_wait();
   const int lane = threadIdx.x & 31;
   const int G = p.s.group, hq = p.s.n_kv_heads * G;
-  const int64_t m64 = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);  // row of the (b, g)
+  const int64_t m64 = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);  // token * G + head
   const int row = blockIdx.y, b = row / p.s.n_kv_heads, g = row % p.s.n_kv_heads;
   if (m64 >= (int64_t)span_qlen(p.s, b) * G) return;
-  const int m = (int)m64;
-  const float* base = p.part + ((int64_t)row * p.tiles_max + m / kPrRows) * p.splits * kPrPart;
-  const int rr = m % kPrRows;
+  const int m = (int)m64, tt = pr_tokens(G), j = m / G;
+  const float* base = p.part + ((int64_t)row * p.tiles_max + j / (2 * tt)) * p.splits * kPrPart;
+  const int jj = j % (2 * tt), rr = jj / tt * 128 + jj % tt * G + m % G;
   float ms = -INFINITY, ls = 0.0f;
   if (lane < p.splits) {
     ms = __ldcg(base + lane * kPrPart + rr);
