@@ -16,7 +16,7 @@
 //    O_B += P_B V, S_B' = Q_B K' (K' the next block): while one tile's
 //    softmax runs, the tensor core works for the other;
 //  - warp 9: K and V blocks into a ring of 32 KB stages, and rotated queries;
-//  - warps 12-15, only where queries are rotated here: the next item's.
+//  - warps 10-15, only where queries are rotated here: the next item's.
 // Everything one thread issues to the tensor core runs in issue order, so S_A'
 // may overwrite P_A without a wait, and S_A' done implies O_A is complete.
 //
@@ -45,6 +45,7 @@ constexpr int kPrRows = 256;             // query rows per item (two tiles)
 // Queries given rotated: three warpgroups, registers 200 + 200 + 104 = 3 * 168;
 // rotated here: four, 184 + 184 + 72 + 72 = 4 * 128.
 __host__ __device__ constexpr int pr_threads(int terms) { return terms == 1 ? 384 : 512; }
+constexpr int kPrRotate = 6;  // warps that rotate queries: the last ones
 // Tokens of a row tile.
 __host__ __device__ constexpr int pr_tokens(int group) { return 128 / group; }
 constexpr int kPrBlock = 128;            // slots per block
@@ -84,30 +85,51 @@ struct PrItem {
   int i0, i1;        // this split's blocks
 };
 
-__device__ __forceinline__ PrItem pr_item(const PromptParams& p, int it) {
+// Where P begins in a tile's S columns: 64 columns, two bf16 each.
+constexpr uint32_t kPrP = 64;
+
+// What a role remembers of the sequence it read last: consecutive items are
+// mostly of one sequence, and its lengths are two dependent loads.
+struct PrSeq {
+  int b, L, nq;
+  int64_t pos0;
+};
+
+__device__ __forceinline__ PrItem pr_item(const PromptParams& p, int it, PrSeq& sq) {
   PrItem w;
   w.valid = false;
-  const int grid = gridDim.x, c = blockIdx.x;
-  const int64_t n64 = (int64_t)it * grid + ((it & 1) ? grid - 1 - c : c);
-  if (n64 >= p.n_items) {
-    w.b = -1;  // past the end
+  const unsigned grid = gridDim.x, c = blockIdx.x;
+  const unsigned n = (unsigned)it * grid + ((it & 1) ? grid - 1 - c : c);  // n_items + grid < 2^31
+  if (n >= (unsigned)p.n_items) {
+    w.b = -1;  // past the end (n grows with `it`, but for the turn of one row)
     return w;
   }
-  const int n = (int)n64;
-  const int rows = p.s.batch * p.s.n_kv_heads, G = p.s.group;
-  w.split = n % p.splits;
-  const int r = (n / p.splits) % rows, k = n / (p.splits * rows);
-  w.b = r / p.s.n_kv_heads;
-  w.g = r % p.s.n_kv_heads;
-  w.L = span_len(p.s, w.b);
-  const int nq = span_qlen(p.s, w.b);
-  w.pos0 = span_pos0(p.s, w.b, w.L, nq);
-  const int per = 2 * pr_tokens(G), tiles = (nq + per - 1) / per;
+  const unsigned rows = p.s.batch * p.s.n_kv_heads;
+  const int G = p.s.group;
+  unsigned rk = n;
+  w.split = 0;
+  if (p.splits > 1) {
+    rk = n / (unsigned)p.splits;
+    w.split = (int)(n - rk * p.splits);
+  }
+  const int k = (int)(rk / rows);
+  const unsigned r = rk - k * rows;
+  w.b = (int)(r / (unsigned)p.s.n_kv_heads);
+  w.g = (int)(r - w.b * p.s.n_kv_heads);
+  if (w.b != sq.b) {
+    sq.b = w.b;
+    sq.L = span_len(p.s, w.b);
+    sq.nq = span_qlen(p.s, w.b);
+    sq.pos0 = span_pos0(p.s, w.b, sq.L, sq.nq);
+  }
+  w.L = sq.L;
+  w.pos0 = sq.pos0;
+  const int per = 2 * pr_tokens(G), tiles = (sq.nq + per - 1) / per;
   if (k >= tiles) return w;
   w.valid = true;
   w.tile = tiles - 1 - k;
   w.j0 = w.tile * per;
-  w.n_tok = min(per, nq - w.j0);
+  w.n_tok = min(per, sq.nq - w.j0);
   const int64_t pa = w.pos0 + w.j0, pb = pa + w.n_tok - 1;
   // the union over positions pa .. pb: the last position's end, the first
   // one's window; its sinks are slots below lo, the rest is inside anyway
@@ -117,8 +139,12 @@ __device__ __forceinline__ PrItem pr_item(const PromptParams& p, int it) {
   w.all.lo = min(first.lo, last.hi);
   w.all.s = min(last.s, w.all.lo);
   w.u = span_units(w.all, kPrBlock);
-  w.i0 = (int)((int64_t)w.u.n * w.split / p.splits);
-  w.i1 = (int)((int64_t)w.u.n * (w.split + 1) / p.splits);
+  w.i0 = 0;
+  w.i1 = w.u.n;
+  if (p.splits > 1) {  // u.n * splits < 2^30 / 128 * 32
+    w.i0 = (int)((unsigned)(w.u.n * w.split) / (unsigned)p.splits);
+    w.i1 = (int)((unsigned)(w.u.n * (w.split + 1)) / (unsigned)p.splits);
+  }
   return w;
 }
 
@@ -223,6 +249,16 @@ __device__ __forceinline__ void pr_ld_wait(uint32_t* r) {
                  "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
                :
                : "memory");
+}
+// 16 columns, waited for.
+__device__ __forceinline__ void pr_ld16(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
 }
 __device__ __forceinline__ void pr_st16(uint32_t taddr, const uint32_t* r) {
   asm volatile(
@@ -352,36 +388,110 @@ struct PrRow {
   Span v;       // the slots it sees
 };
 
-// One block of a row tile: S out of tensor memory, P into it, m_ref, l and O
-// brought along. FULL: all four 32-column chunks take part, else [ca, cb).
-// bad: the block's pages outside the pool.
-template <bool FULL>
-__device__ __forceinline__ void pr_softmax(PrRow& row, uint32_t t_s, uint32_t t_o, int t0, int ca, int cb, bool first,
-                                           unsigned bad, int log2bs) {
-  constexpr float c = 1.4426950408889634f * 0.08838834764831845f;  // log2(e) / sqrt(128)
-  auto on = [&](int q) { return FULL || (q >= ca && q < cb); };
-  // S is read twice, for the maximum and for the exponentials: 32 columns at
-  // a time in registers, the next 32 on their way
-  const bool whole = t0 + kPrBlock <= row.v.hi && (t0 >= row.v.lo || t0 + kPrBlock <= row.v.s);
-  const bool masked = __any_sync(0xFFFFFFFFu, !whole) || bad;
-  uint32_t ms[4] = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};
-  if (masked) {
+// The reference follows the block's maximum m_blk where that has outgrown it;
+// O and l with it.
+__device__ __forceinline__ void pr_follow(PrRow& row, float m_blk, uint32_t t_o, bool first) {
+  if (m_blk != m_blk) row.l = m_blk;  // a NaN logit
+  const bool grow = m_blk > row.m_ref + 8.0f || (row.m_ref == -INFINITY && m_blk > -INFINITY);
+  if (!__any_sync(0xFFFFFFFFu, grow)) return;
+  const float m_new = grow ? m_blk : row.m_ref;
+  const float f = row.m_ref == -INFINITY ? 0.0f : pr_ex2(row.m_ref - m_new);
+  if (!first && __any_sync(0xFFFFFFFFu, grow && row.m_ref > -INFINITY)) {
+    const float fo = grow ? f : 1.0f;
+#pragma unroll 1
+    for (int q = 0; q < 8; ++q) {
+      uint32_t o[16];
+      pr_ld16(t_o + q * 16, o);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      ms[q] = pr_mask(row.v, t0, q);
-      if (bad)
-        for (int e = 0; e < 32; ++e)
-          if ((bad >> min((q * 32 + e) >> log2bs, 31)) & 1u) ms[q] &= ~(1u << e);
+      for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fo);
+      pr_st16(t_o + q * 16, o);
     }
   }
-  auto hide = [&](uint32_t* s, int q) {
-    if (masked) {
+  if (grow) {
+    row.l *= f;
+    row.m_ref = m_new;
+  }
+}
+// 32 columns' P (as 16 words) and its part of the sum; x2 = s c2 + off2.
+__device__ __forceinline__ void pr_probs(const uint32_t* s, uint32_t* pk, uint64_t c2, uint64_t off2, uint64_t (&ls)[2]) {
 #pragma unroll
-      for (int e = 0; e < 32; ++e)
-        if (!((ms[q] >> e) & 1u)) s[e] = 0xFF800000u;  // -inf
+  for (int e = 0; e < 16; ++e) {
+    const uint64_t x = pr_fma2(pr_two(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), c2, off2);
+    float2 y;
+    if ((e & 7) < kPrFmaPairs) {
+      y = pr_exp2_fma(x);
+    } else {
+      y = pr_both(x);
+      y = make_float2(pr_ex2(y.x), pr_ex2(y.y));
     }
-  };
+    ls[e & 1] = pr_add2(ls[e & 1], pr_two(y.x, y.y));
+    pk[e] = tc_pack(y.x, y.y);
+  }
+}
+__device__ __forceinline__ float pr_top(const uint32_t* s, int n) {
   float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int e = 0; e < n; e += 2)
+    mx[(e >> 1) & 3] = pr_max3(mx[(e >> 1) & 3], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+  return pr_max(pr_max(mx[0], mx[1]), pr_max(mx[2], mx[3]));
+}
+constexpr float kPrScale = 1.4426950408889634f * 0.08838834764831845f;  // log2(e) / sqrt(128)
+
+// One block of a row tile that every row sees whole: S out of tensor memory, P
+// into it, m_ref, l and O brought along. After the maximum, columns 64 .. 127
+// are still in registers and go first; 0 .. 63 are read again meanwhile. P
+// takes the place of S's columns 64 .. 127 (kPrP).
+__device__ __forceinline__ void pr_softmax_whole(PrRow& row, uint32_t t_s, uint32_t t_o, bool first) {
+  uint32_t a[64], b[64], pk[32];
+  pr_ld32(t_s, b);
+  pr_ld32(t_s + 32, b + 32);
+  pr_ld32(t_s + 64, a);
+  pr_ld32(t_s + 96, a + 32);
+  pr_ld_wait(b);
+  pr_ld_wait(b + 32);
+  pr_ld_wait(a);
+  pr_ld_wait(a + 32);
+  pr_follow(row, pr_max(pr_top(b, 64), pr_top(a, 64)) * kPrScale, t_o, first);
+  const float off = row.m_ref == -INFINITY ? 0.0f : -row.m_ref;
+  const uint64_t c2 = pr_two(kPrScale, kPrScale), off2 = pr_two(off, off);
+  uint64_t ls[2] = {0, 0};
+  pr_ld32(t_s, b);
+  pr_probs(a, pk, c2, off2, ls);
+  pr_probs(a + 32, pk + 16, c2, off2, ls);
+  pr_ld_wait(b);
+  pr_ld32(t_s + 32, b + 32);
+  pr_st16(t_s + kPrP + 32, pk);
+  pr_st16(t_s + kPrP + 48, pk + 16);
+  pr_probs(b, pk, c2, off2, ls);
+  pr_ld_wait(b + 32);
+  pr_st16(t_s + kPrP, pk);
+  pr_probs(b + 32, pk, c2, off2, ls);
+  pr_st16(t_s + kPrP + 16, pk);
+  const float2 y = pr_both(pr_add2(ls[0], ls[1]));
+  row.l += y.x + y.y;
+}
+
+// The same for chunks [ca, cb) under the rows' masks. bad: the block's pages
+// outside the pool.
+__device__ __forceinline__ void pr_softmax_part(PrRow& row, uint32_t t_s, uint32_t t_o, int t0, int ca, int cb, bool first,
+                                           unsigned bad, int log2bs) {
+  auto on = [&](int q) { return q >= ca && q < cb; };
+  // S is read twice, for the maximum and for the exponentials: 32 columns at
+  // a time in registers, the next 32 on their way
+  uint32_t ms[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    ms[q] = pr_mask(row.v, t0, q);
+    if (bad)
+      for (int e = 0; e < 32; ++e)
+        if ((bad >> min((q * 32 + e) >> log2bs, 31)) & 1u) ms[q] &= ~(1u << e);
+  }
+  auto hide = [&](uint32_t* s, int q) {
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      if (!((ms[q] >> e) & 1u)) s[e] = 0xFF800000u;  // -inf
+  };
+  float mx = -INFINITY;
   uint32_t sa[32], sb[32];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -391,65 +501,30 @@ __device__ __forceinline__ void pr_softmax(PrRow& row, uint32_t t_s, uint32_t t_
       if (!on(q)) return;
       pr_ld_wait(s);
       hide(s, q);
-#pragma unroll
-      for (int e = 0; e < 32; e += 2)
-        mx[(e >> 1) & 3] = pr_max3(mx[(e >> 1) & 3], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+      mx = pr_max(mx, pr_top(s, 32));
     };
     top(sa, 2 * h);
     top(sb, 2 * h + 1);
   }
-  if (on(0)) pr_ld32(t_s, sa);
-  const float m_blk = pr_max(pr_max(mx[0], mx[1]), pr_max(mx[2], mx[3])) * c;
-  if (m_blk != m_blk) row.l = m_blk;  // a NaN logit
-  const bool grow = m_blk > row.m_ref + 8.0f || (row.m_ref == -INFINITY && m_blk > -INFINITY);
-  if (__any_sync(0xFFFFFFFFu, grow)) {
-    const float m_new = grow ? m_blk : row.m_ref;
-    const float f = row.m_ref == -INFINITY ? 0.0f : pr_ex2(row.m_ref - m_new);
-    if (!first && __any_sync(0xFFFFFFFFu, grow && row.m_ref > -INFINITY)) {
-      const float fo = grow ? f : 1.0f;
-#pragma unroll 1
-      for (int q = 0; q < 4; ++q) {
-        pr_ld32(t_o + q * 32, sb);
-        pr_ld_wait(sb);
-#pragma unroll
-        for (int e = 0; e < 32; ++e) sb[e] = __float_as_uint(__uint_as_float(sb[e]) * fo);
-        pr_st16(t_o + q * 32, sb);
-        pr_st16(t_o + q * 32 + 16, sb + 16);
-      }
-    }
-    if (grow) {
-      row.l *= f;
-      row.m_ref = m_new;
-    }
-  }
+  pr_follow(row, mx * kPrScale, t_o, first);
+  // downwards: P of a chunk takes the place of columns that are read by then
+  if (on(3)) pr_ld32(t_s + 96, sa);
   const float off = row.m_ref == -INFINITY ? 0.0f : -row.m_ref;
-  const uint64_t c2 = pr_two(c, c), off2 = pr_two(off, off);
+  const uint64_t c2 = pr_two(kPrScale, kPrScale), off2 = pr_two(off, off);
   uint64_t ls[2] = {0, 0};
   auto probs = [&](uint32_t* s, uint32_t* ahead, int q) {
     if (on(q)) pr_ld_wait(s);
-    if (q < 3 && on(q + 1)) pr_ld32(t_s + (q + 1) * 32, ahead);
+    if (q > 0 && on(q - 1)) pr_ld32(t_s + (q - 1) * 32, ahead);
     if (!on(q)) return;
     hide(s, q);
     uint32_t pk[16];
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const uint64_t x = pr_fma2(pr_two(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), c2, off2);
-      float2 y;
-      if ((e & 7) < kPrFmaPairs) {
-        y = pr_exp2_fma(x);
-      } else {
-        y = pr_both(x);
-        y = make_float2(pr_ex2(y.x), pr_ex2(y.y));
-      }
-      ls[e & 1] = pr_add2(ls[e & 1], pr_two(y.x, y.y));
-      pk[e] = tc_pack(y.x, y.y);
-    }
-    pr_st16(t_s + q * 16, pk);
+    pr_probs(s, pk, c2, off2, ls);
+    pr_st16(t_s + kPrP + q * 16, pk);
   };
-  probs(sa, sb, 0);
-  probs(sb, sa, 1);
-  probs(sa, sb, 2);
-  probs(sb, sa, 3);
+  probs(sa, sb, 3);
+  probs(sb, sa, 2);
+  probs(sa, sb, 1);
+  probs(sb, sa, 0);
   const float2 a = pr_both(pr_add2(ls[0], ls[1]));
   row.l += a.x + a.y;
 }
@@ -483,7 +558,7 @@ __global__ void __launch_bounds__(pr_threads(TERMS), 1) span_prompt_kernel(const
       mbar_init(bar_s + i, 1);
       mbar_init(bar_p + i, 128);
       mbar_init(bar_o + i, 1);
-      mbar_init(bar_q + i, TERMS == 1 ? 1 : 128);
+      mbar_init(bar_q + i, TERMS == 1 ? 1 : kPrRotate * 32);
       mbar_init(bar_f + i, 1);
     }
     fence_mbar_init();
@@ -515,11 +590,13 @@ __global__ void __launch_bounds__(pr_threads(TERMS), 1) span_prompt_kernel(const
     auto out_row = [&](const PrItem& w) {  // row of out [B n_q Hq][128]
       return ((int64_t)w.b * p.s.n_q + w.j0 + sub * tt + rt) * hq + w.g * G + rh;
     };
+    PrSeq sq;
+    sq.b = -1;
     // the next item with blocks, from `it` on; items without get their zeros
     // on the way
     auto next = [&](int& it, PrItem& w) -> bool {
       for (;; ++it) {
-        w = pr_item(p, it);
+        w = pr_item(p, it, sq);
         if (w.b < 0) return false;
         if (!w.valid) continue;
         if (w.i0 < w.i1) return true;
@@ -565,10 +642,11 @@ __global__ void __launch_bounds__(pr_threads(TERMS), 1) span_prompt_kernel(const
           }
           ++n_s;
           tc_fence_after();
-          if (cb - ca == 4)
-            pr_softmax<true>(row, t_s, t_o, t0, 0, 4, i == w.i0, bad, p.s.pm.log2bs);
+          const bool whole = t0 + kPrBlock <= row.v.hi && (t0 >= row.v.lo || t0 + kPrBlock <= row.v.s);
+          if (cb - ca == 4 && !bad && __all_sync(0xFFFFFFFFu, whole || !mine))
+            pr_softmax_whole(row, t_s, t_o, i == w.i0);
           else
-            pr_softmax<false>(row, t_s, t_o, t0, ca, cb, i == w.i0, bad, p.s.pm.log2bs);
+            pr_softmax_part(row, t_s, t_o, t0, ca, cb, i == w.i0, bad, p.s.pm.log2bs);
           pr_st_wait();
           tc_fence_before();
           pr_arrive(bar_p + sub);
@@ -576,6 +654,8 @@ __global__ void __launch_bounds__(pr_threads(TERMS), 1) span_prompt_kernel(const
         if (!ok) break;
         const int64_t at = mine ? out_row(w) : -1;
         float* pp = p.splits > 1 ? part_of(w) : nullptr;
+        ++it;
+        more = next(it, w);
         if (!pr_wait(bar_o + sub, n_o & 1)) {
           ok = false;
           break;
@@ -625,9 +705,10 @@ __global__ void __launch_bounds__(pr_threads(TERMS), 1) span_prompt_kernel(const
           }
         }
         tc_fence_before();
+      } else {
+        ++it;
+        more = next(it, w);
       }
-      ++it;
-      more = next(it, w);
     }
   } else if (TERMS == 1) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
@@ -638,6 +719,8 @@ __global__ void __launch_bounds__(pr_threads(TERMS), 1) span_prompt_kernel(const
     // ----------------------------------------------------- the products
     uint32_t kv = 0, n_p[2] = {0, 0}, n_q[2] = {0, 0};
     bool ok = true;
+    PrSeq sq;
+    sq.b = -1;
     // low descriptor words of Q of tile A, of a block as K (rows of chunk 0),
     // as V (64-dim halves 16 KB apart)
     const uint32_t tb = pr_uni(tbase);
@@ -658,7 +741,7 @@ __global__ void __launch_bounds__(pr_threads(TERMS), 1) span_prompt_kernel(const
       __syncwarp();
     };
     for (int it = 0; ok; ++it) {
-      const PrItem w = pr_item(p, it);
+      const PrItem w = pr_item(p, it, sq);
       if (w.b < 0) break;
       if (!w.valid || w.i0 >= w.i1) continue;
       const int subs = w.n_tok > tt ? 2 : 1;
@@ -699,7 +782,7 @@ __global__ void __launch_bounds__(pr_threads(TERMS), 1) span_prompt_kernel(const
           if (!(ok = pr_wait(bar_p + sub, n_p[sub]++ & 1))) break;
           tc_fence_after();
           {
-            const uint32_t d = pr_uni(tb + 256 + sub * 128), pa = pr_uni(tb + sub * 128),
+            const uint32_t d = pr_uni(tb + 256 + sub * 128), pa = pr_uni(tb + sub * 128 + kPrP),
                            v = pr_uni(v_lo + vs_st * (kPrTile >> 4));
             if (pr_elect()) {
               if (cb - ca == 4)
@@ -724,6 +807,8 @@ __global__ void __launch_bounds__(pr_threads(TERMS), 1) span_prompt_kernel(const
     // ------------------------------------------------------- the loads
     uint32_t n = 0, n_f[2] = {0, 0};
     bool ok = true;
+    PrSeq sq;
+    sq.b = -1;
     const int boxes = kPrBlock / p.box_rows;
     auto load = [&](const PrItem& w, int i, bool is_v) {
       const uint32_t st = n % kStages;
@@ -751,7 +836,7 @@ __global__ void __launch_bounds__(pr_threads(TERMS), 1) span_prompt_kernel(const
       ++n;
     };
     for (int it = 0; ok; ++it) {
-      const PrItem w = pr_item(p, it);
+      const PrItem w = pr_item(p, it, sq);
       if (w.b < 0) break;
       if (!w.valid) continue;
       for (int i = w.i0; i < w.i1 && ok; ++i) {
@@ -782,28 +867,30 @@ __global__ void __launch_bounds__(pr_threads(TERMS), 1) span_prompt_kernel(const
     if (TERMS == 1)
       for (int sub = 0; sub < 2; ++sub)
         if (n_f[sub] > 0) mbar_wait(bar_q + sub, (n_f[sub] - 1) & 1);
-  } else if (TERMS == 2 && warp >= 12) {
+  } else if (TERMS == 2 && warp >= 16 - kPrRotate) {
     // ---------------------------------------------- rotated queries, two terms
     uint32_t n_f[2] = {0, 0};
     bool ok = true;
+    PrSeq sq;
+    sq.b = -1;
     const __nv_bfloat16* qg = static_cast<const __nv_bfloat16*>(p.s.q);
     const int ch = lane & 7;  // 8 lanes a token, each the chunks ch and ch + 8 (dims i and i + 64 of 8 FCs)
     for (int it = 0; ok; ++it) {
-      const PrItem w = pr_item(p, it);
+      const PrItem w = pr_item(p, it, sq);
       if (w.b < 0) break;
       if (!w.valid || w.i0 >= w.i1) continue;
       for (int sub = 0; sub < 2 && sub * tt < w.n_tok; ++sub) {
         unsigned char* qs = smem + sub * TERMS * kPrTile;
-        const int jt0 = (warp & 3) * 4 + (lane >> 3), n_t = min(tt, w.n_tok - sub * tt);
+        const int wq = warp - (16 - kPrRotate), n_t = min(tt, w.n_tok - sub * tt);
         const __nv_bfloat16* base = qg + (((int64_t)w.b * p.s.n_q + w.j0 + sub * tt) * hq + w.g * G) * kD;
-        for (int e = (warp & 3) * 32 + lane; e < n_t * 2 * G; e += 128)  // on their way to L2 meanwhile
+        for (int e = wq * 32 + lane; e < n_t * 2 * G; e += kPrRotate * 32)  // on their way to L2 meanwhile
           prefetch_line_l2(base + (int64_t)(e / (2 * G)) * hq * kD + (e % (2 * G)) * 64);
         if (n_f[sub] > 0 && !pr_wait(bar_f + sub, (n_f[sub] - 1) & 1)) {
           ok = false;
           break;
         }
         ++n_f[sub];
-        for (int jt = jt0; jt < n_t; jt += 16) {
+        for (int jt = wq * 4 + (lane >> 3); jt < n_t; jt += 4 * kPrRotate) {
           float cs[8], sn[8];  // an angle serves the G heads
 #pragma unroll
           for (int e = 0; e < 8; ++e) span_angle(turns[ch * 8 + e], w.pos0 + w.j0 + sub * tt + jt, cs + e, sn + e);
