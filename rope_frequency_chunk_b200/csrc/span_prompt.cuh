@@ -208,23 +208,20 @@ __device__ __forceinline__ void pr_issue_s(uint32_t d, uint32_t q, uint32_t k, u
         pr_mma_ss<true>(d, pr_desc(q + t * (kPrTile >> 4) + o), pr_desc(k + o), idesc);
     }
 }
-// O (+)= P V over K-steps [2 ca, 2 cb) of 16 slots.
-template <bool FULL>
-__device__ __forceinline__ void pr_issue_o(uint32_t d, uint32_t pa, uint32_t v, int ca, int cb, bool acc) {
-  if (FULL) {
-    if (acc)
-      pr_mma_ts<true>(d, pa, pr_desc(v), tc_idesc(1));
-    else
-      pr_mma_ts<false>(d, pa, pr_desc(v), tc_idesc(1));
+// O (+)= P V over four K-steps of 16 slots from k0 on, or over [2 ca, 2 cb).
+template <bool ACC>
+__device__ __forceinline__ void pr_issue_o(uint32_t d, uint32_t pa, uint32_t v, int k0) {
+  pr_mma_ts<ACC>(d, pa + k0 * 8, pr_desc(v + k0 * (2048 >> 4)), tc_idesc(1));
 #pragma unroll
-    for (int k8 = 1; k8 < 8; ++k8) pr_mma_ts<true>(d, pa + k8 * 8, pr_desc(v + k8 * (2048 >> 4)), tc_idesc(1));
-  } else {
-    for (int k8 = 2 * ca; k8 < 2 * cb; ++k8) {
-      if (acc || k8 > 2 * ca)
-        pr_mma_ts<true>(d, pa + k8 * 8, pr_desc(v + k8 * (2048 >> 4)), tc_idesc(1));
-      else
-        pr_mma_ts<false>(d, pa + k8 * 8, pr_desc(v + k8 * (2048 >> 4)), tc_idesc(1));
-    }
+  for (int k8 = 1; k8 < 4; ++k8)
+    pr_mma_ts<true>(d, pa + (k0 + k8) * 8, pr_desc(v + (k0 + k8) * (2048 >> 4)), tc_idesc(1));
+}
+__device__ __forceinline__ void pr_issue_part(uint32_t d, uint32_t pa, uint32_t v, int ca, int cb, bool acc) {
+  for (int k8 = 2 * ca; k8 < 2 * cb; ++k8) {
+    if (acc || k8 > 2 * ca)
+      pr_mma_ts<true>(d, pa + k8 * 8, pr_desc(v + k8 * (2048 >> 4)), tc_idesc(1));
+    else
+      pr_mma_ts<false>(d, pa + k8 * 8, pr_desc(v + k8 * (2048 >> 4)), tc_idesc(1));
   }
 }
 __device__ __forceinline__ void pr_ld32(uint32_t taddr, uint32_t* r) {
@@ -326,6 +323,13 @@ __device__ __forceinline__ float2 pr_exp2_fma(uint64_t x2) {
 // Of every eight pairs of a row, this many take pr_exp2_fma.
 constexpr int kPrFmaPairs = 2;
 
+// One arrival for the warp, behind its tensor-memory stores.
+__device__ __forceinline__ void pr_stored(uint64_t* bar, int lane) {
+  pr_st_wait();
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) pr_arrive(bar);
+}
 __device__ __forceinline__ float pr_ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -441,7 +445,8 @@ constexpr float kPrScale = 1.4426950408889634f * 0.08838834764831845f;  // log2(
 // into it, m_ref, l and O brought along. After the maximum, columns 64 .. 127
 // are still in registers and go first; 0 .. 63 are read again meanwhile. P
 // takes the place of S's columns 64 .. 127 (kPrP).
-__device__ __forceinline__ void pr_softmax_whole(PrRow& row, uint32_t t_s, uint32_t t_o, bool first) {
+__device__ __forceinline__ void pr_softmax_whole(PrRow& row, uint32_t t_s, uint32_t t_o, bool first, uint64_t* half,
+                                                 int lane) {
   uint32_t a[64], b[64], pk[32];
   pr_ld32(t_s, b);
   pr_ld32(t_s + 32, b + 32);
@@ -464,6 +469,7 @@ __device__ __forceinline__ void pr_softmax_whole(PrRow& row, uint32_t t_s, uint3
   pr_st16(t_s + kPrP + 48, pk + 16);
   pr_probs(b, pk, c2, off2, ls);
   pr_ld_wait(b + 32);
+  pr_stored(half, lane);
   pr_st16(t_s + kPrP, pk);
   pr_probs(b + 32, pk, c2, off2, ls);
   pr_st16(t_s + kPrP + 16, pk);
@@ -541,7 +547,8 @@ __global__ void __launch_bounds__(pr_threads(TERMS), 1) span_prompt_kernel(const
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + SM::kBars);  // [kStages]
   uint64_t* empty = full + kStages;                                // [kStages]
   uint64_t* bar_s = empty + kStages;  // [2] S of a tile is ready
-  uint64_t* bar_p = bar_s + 2;        // [2] P is in tensor memory
+  uint64_t* bar_h = bar_s + 2;        // [2] P of a block's columns 64 .. 127 is in tensor memory
+  uint64_t* bar_p = bar_h + 2;        // [2] all of P is
   uint64_t* bar_o = bar_p + 2;        // [2] an item's O is complete
   uint64_t* bar_q = bar_o + 2;        // [2] an item's Q is staged
   uint64_t* bar_f = bar_q + 2;        // [2] an item's Q is no longer read
@@ -556,7 +563,8 @@ __global__ void __launch_bounds__(pr_threads(TERMS), 1) span_prompt_kernel(const
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar_s + i, 1);
-      mbar_init(bar_p + i, 128);
+      mbar_init(bar_h + i, 4);
+      mbar_init(bar_p + i, 4);
       mbar_init(bar_o + i, 1);
       mbar_init(bar_q + i, TERMS == 1 ? 1 : kPrRotate * 32);
       mbar_init(bar_f + i, 1);
@@ -643,13 +651,13 @@ __global__ void __launch_bounds__(pr_threads(TERMS), 1) span_prompt_kernel(const
           ++n_s;
           tc_fence_after();
           const bool whole = t0 + kPrBlock <= row.v.hi && (t0 >= row.v.lo || t0 + kPrBlock <= row.v.s);
-          if (cb - ca == 4 && !bad && __all_sync(0xFFFFFFFFu, whole || !mine))
-            pr_softmax_whole(row, t_s, t_o, i == w.i0);
-          else
+          if (cb - ca == 4 && !bad && __all_sync(0xFFFFFFFFu, whole || !mine)) {
+            pr_softmax_whole(row, t_s, t_o, i == w.i0, bar_h + sub, lane);
+          } else {
             pr_softmax_part(row, t_s, t_o, t0, ca, cb, i == w.i0, bad, p.s.pm.log2bs);
-          pr_st_wait();
-          tc_fence_before();
-          pr_arrive(bar_p + sub);
+            pr_stored(bar_h + sub, lane);
+          }
+          pr_stored(bar_p + sub, lane);
         }
         if (!ok) break;
         const int64_t at = mine ? out_row(w) : -1;
@@ -779,21 +787,30 @@ __global__ void __launch_bounds__(pr_threads(TERMS), 1) span_prompt_kernel(const
         int na = 0, nb = 1;  // the next block's chunks
         if (!last) pr_chunks(w.all, w.u.unit(i + 1) * kPrBlock, na, nb);
         for (int sub = 0; sub < subs && ok; ++sub) {
-          if (!(ok = pr_wait(bar_p + sub, n_p[sub]++ & 1))) break;
+          const uint32_t d = pr_uni(tb + 256 + sub * 128), pa = pr_uni(tb + sub * 128 + kPrP),
+                         v = pr_uni(v_lo + vs_st * (kPrTile >> 4));
+          if (!(ok = pr_wait(bar_h + sub, n_p[sub] & 1))) break;
           tc_fence_after();
-          {
-            const uint32_t d = pr_uni(tb + 256 + sub * 128), pa = pr_uni(tb + sub * 128 + kPrP),
-                           v = pr_uni(v_lo + vs_st * (kPrTile >> 4));
+          if (cb - ca == 4) {  // the upper half while the lower is still computed
             if (pr_elect()) {
-              if (cb - ca == 4)
-                pr_issue_o<true>(d, pa, v, 0, 4, i > w.i0);
+              if (i > w.i0)
+                pr_issue_o<true>(d, pa, v, 4);
               else
-                pr_issue_o<false>(d, pa, v, ca, cb, i > w.i0);
-              if (last) tc_commit(bar_o + sub);
-              if (sub == subs - 1) tc_commit(empty + vs_st);
+                pr_issue_o<false>(d, pa, v, 4);
             }
             __syncwarp();
           }
+          if (!(ok = pr_wait(bar_p + sub, n_p[sub]++ & 1))) break;
+          tc_fence_after();
+          if (pr_elect()) {
+            if (cb - ca == 4)
+              pr_issue_o<true>(d, pa, v, 0);
+            else
+              pr_issue_part(d, pa, v, ca, cb, i > w.i0);
+            if (last) tc_commit(bar_o + sub);
+            if (sub == subs - 1) tc_commit(empty + vs_st);
+          }
+          __syncwarp();
           if (!last) {
             if (sub == 0 && !(ok = wait_full(k_n))) break;
             issue_s(sub, k_n % kStages, na, nb, i + 2 == w.i1, sub == subs - 1);
