@@ -170,7 +170,7 @@ fasa_status launch_prompt_t(const PromptParams& p, int grid, cudaStream_t st) {
     return cuda_status(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
   });
   if (s != FASA_OK) return s;
-  return launch_pdl(kern, dim3((unsigned)grid, 1, 1), pr_threads(TERMS), smem, st, p);
+  return launch_pdl(kern, dim3((unsigned)grid, 1, 1), kPrThreads, smem, st, p);
 }
 
 fasa_status launch_prompt(const fasa_cache* c, const fasa_paged* pg, const fasa_span* sp, const void* q, int32_t n_q,

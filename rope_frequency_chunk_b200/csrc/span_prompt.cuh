@@ -9,14 +9,18 @@
 // The CTAs (one per SM) walk the items, the longest first.
 //
 // Roles in a CTA (the softmax warps take registers from the others):
-//  - warps 0-3 and 4-7: the softmax of row tile A and B, one row per thread:
-//    S row from tensor memory, mask, running maximum and sum, P as bf16 into
-//    the tensor memory of S; at the end of an item its output;
-//  - warp 8: issues the products. Per block: O_A += P_A V, S_A' = Q_A K',
+//  - warps 0-15: the softmax, two threads per row: warps 0-3 columns 0-63 of
+//    tile A's S, 4-7 columns 64-127, 8-15 tile B. S from tensor memory, mask,
+//    maximum (the two threads exchange theirs through shared memory), running
+//    sum, P as bf16 into the tensor memory of S; at the end of an item half of
+//    its output row each, and the next item's queries where they are rotated
+//    here. With one thread per row the softmax of a tile (about 1400 cycles)
+//    and its products (about 1100, half of them latency) made a chain that
+//    kept the tensor core idle for more than a third of the time;
+//  - warp 16: issues the products. Per block: O_A += P_A V, S_A' = Q_A K',
 //    O_B += P_B V, S_B' = Q_B K' (K' the next block): while one tile's
 //    softmax runs, the tensor core works for the other;
-//  - warp 9: K and V blocks into a ring of 32 KB stages, and rotated queries;
-//  - warps 10-15, only where queries are rotated here: the next item's.
+//  - warp 17: K and V blocks into a ring of 32 KB stages, and rotated queries.
 // Everything one thread issues to the tensor core runs in issue order, so S_A'
 // may overwrite P_A without a wait, and S_A' done implies O_A is complete.
 //
@@ -42,10 +46,7 @@
 namespace fasa {
 
 constexpr int kPrRows = 256;             // query rows per item (two tiles)
-// Queries given rotated: three warpgroups, registers 200 + 200 + 104 = 3 * 168;
-// rotated here: four, 184 + 184 + 72 + 72 = 4 * 128.
-__host__ __device__ constexpr int pr_threads(int terms) { return terms == 1 ? 384 : 512; }
-constexpr int kPrRotate = 6;  // warps that rotate queries: the last ones
+constexpr int kPrThreads = 640;          // five warpgroups; registers 4 * 104 + 64 = 5 * 96
 // Tokens of a row tile.
 __host__ __device__ constexpr int pr_tokens(int group) { return 128 / group; }
 constexpr int kPrBlock = 128;            // slots per block
@@ -72,7 +73,10 @@ struct PrSmem {
   static constexpr int kStages = TERMS == 1 ? 5 : 3;
   static constexpr uint32_t kQ = 2 * TERMS * kPrTile;  // tile A's terms, tile B's terms
   static constexpr uint32_t kBars = kQ + kStages * kPrTile;
-  static constexpr uint32_t kBytes = kBars + 256 + 1024;  // barriers; alignment to 1024
+  static constexpr uint32_t kPair = kBars + 256;          // [2 tiles][2 halves][128 rows] f32
+  static constexpr uint32_t kTurns = kPair + 2048;
+  static constexpr uint32_t kBytes = kTurns + (TERMS == 2 ? kNFC * 8 : 0);  // no static shared memory: the base is
+                                                                            // 1024-byte aligned (checked)
 };
 
 // One item as every role sees it.
@@ -85,8 +89,8 @@ struct PrItem {
   int i0, i1;        // this split's blocks
 };
 
-// Where P begins in a tile's S columns: 64 columns, two bf16 each.
-constexpr uint32_t kPrP = 64;
+// P of a half's 64 columns takes the place of the upper 32 of them.
+constexpr uint32_t kPrP = 32;
 
 // What a role remembers of the sequence it read last: consecutive items are
 // mostly of one sequence, and its lengths are two dependent loads.
@@ -101,7 +105,7 @@ __device__ __forceinline__ PrItem pr_item(const PromptParams& p, int it, PrSeq& 
   const unsigned grid = gridDim.x, c = blockIdx.x;
   const unsigned n = (unsigned)it * grid + ((it & 1) ? grid - 1 - c : c);  // n_items + grid < 2^31
   if (n >= (unsigned)p.n_items) {
-    w.b = -1;  // past the end (n grows with `it`, but for the turn of one row)
+    w.b = -1;  // past the end: n grows with `it`
     return w;
   }
   const unsigned rows = p.s.batch * p.s.n_kv_heads;
@@ -208,20 +212,21 @@ __device__ __forceinline__ void pr_issue_s(uint32_t d, uint32_t q, uint32_t k, u
         pr_mma_ss<true>(d, pr_desc(q + t * (kPrTile >> 4) + o), pr_desc(k + o), idesc);
     }
 }
-// O (+)= P V over four K-steps of 16 slots from k0 on, or over [2 ca, 2 cb).
+// Column of P for K-step k8 (16 slots), behind the tile's P base.
+__host__ __device__ constexpr uint32_t pr_pcol(int k8) { return (k8 >> 2) * 64 + (k8 & 3) * 8; }
+// O (+)= P V over the block's eight K-steps, or over [2 ca, 2 cb).
 template <bool ACC>
-__device__ __forceinline__ void pr_issue_o(uint32_t d, uint32_t pa, uint32_t v, int k0) {
-  pr_mma_ts<ACC>(d, pa + k0 * 8, pr_desc(v + k0 * (2048 >> 4)), tc_idesc(1));
+__device__ __forceinline__ void pr_issue_o(uint32_t d, uint32_t pa, uint32_t v) {
+  pr_mma_ts<ACC>(d, pa, pr_desc(v), tc_idesc(1));
 #pragma unroll
-  for (int k8 = 1; k8 < 4; ++k8)
-    pr_mma_ts<true>(d, pa + (k0 + k8) * 8, pr_desc(v + (k0 + k8) * (2048 >> 4)), tc_idesc(1));
+  for (int k8 = 1; k8 < 8; ++k8) pr_mma_ts<true>(d, pa + pr_pcol(k8), pr_desc(v + k8 * (2048 >> 4)), tc_idesc(1));
 }
 __device__ __forceinline__ void pr_issue_part(uint32_t d, uint32_t pa, uint32_t v, int ca, int cb, bool acc) {
   for (int k8 = 2 * ca; k8 < 2 * cb; ++k8) {
     if (acc || k8 > 2 * ca)
-      pr_mma_ts<true>(d, pa + k8 * 8, pr_desc(v + k8 * (2048 >> 4)), tc_idesc(1));
+      pr_mma_ts<true>(d, pa + pr_pcol(k8), pr_desc(v + k8 * (2048 >> 4)), tc_idesc(1));
     else
-      pr_mma_ts<false>(d, pa + k8 * 8, pr_desc(v + k8 * (2048 >> 4)), tc_idesc(1));
+      pr_mma_ts<false>(d, pa + pr_pcol(k8), pr_desc(v + k8 * (2048 >> 4)), tc_idesc(1));
   }
 }
 __device__ __forceinline__ void pr_ld32(uint32_t taddr, uint32_t* r) {
@@ -301,28 +306,6 @@ __device__ __forceinline__ uint64_t pr_add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-// 2^x for x <= 2^20 without the special function unit, whose 16 results a
-// clock are what the softmax waits for: x = n + f with |f| <= 1/2 (n by adding
-// and subtracting 1.5 * 2^23), 2^f by a cubic fitted to the least relative
-// error with 2^0 = 1 exact (error 1.0e-4, a fortieth of P's rounding to bf16),
-// n added to the exponent. x <= -127, and -inf, give 0 exactly.
-__device__ __forceinline__ float2 pr_exp2_fma(uint64_t x2) {
-  float2 x = pr_both(x2);
-  x2 = pr_two(fmaxf(x.x, -127.0f), fmaxf(x.y, -127.0f));
-  const uint64_t big = pr_two(12582912.0f, 12582912.0f), nbig = pr_two(-12582912.0f, -12582912.0f);
-  const uint64_t t = pr_add2(x2, big);
-  const uint64_t f = pr_fma2(pr_add2(t, nbig), pr_two(-1.0f, -1.0f), x2);
-  uint64_t y = pr_fma2(f, pr_two(0.05500893294811249f, 0.05500893294811249f),
-                       pr_two(0.2422109693288803f, 0.2422109693288803f));
-  y = pr_fma2(f, y, pr_two(0.6932829022407532f, 0.6932829022407532f));
-  y = pr_fma2(f, y, pr_two(1.0f, 1.0f));
-  const float2 ti = pr_both(t), yi = pr_both(y);
-  return make_float2(__uint_as_float((__float_as_uint(ti.x) << 23) + __float_as_uint(yi.x)),
-                     __uint_as_float((__float_as_uint(ti.y) << 23) + __float_as_uint(yi.y)));
-}
-// Of every eight pairs of a row, this many take pr_exp2_fma.
-constexpr int kPrFmaPairs = 2;
-
 // One arrival for the warp, behind its tensor-memory stores.
 __device__ __forceinline__ void pr_stored(uint64_t* bar, int lane) {
   pr_st_wait();
@@ -403,7 +386,7 @@ __device__ __forceinline__ void pr_follow(PrRow& row, float m_blk, uint32_t t_o,
   if (!first && __any_sync(0xFFFFFFFFu, grow && row.m_ref > -INFINITY)) {
     const float fo = grow ? f : 1.0f;
 #pragma unroll 1
-    for (int q = 0; q < 8; ++q) {
+    for (int q = 0; q < 4; ++q) {  // this thread's half of the O row
       uint32_t o[16];
       pr_ld16(t_o + q * 16, o);
 #pragma unroll
@@ -421,13 +404,8 @@ __device__ __forceinline__ void pr_probs(const uint32_t* s, uint32_t* pk, uint64
 #pragma unroll
   for (int e = 0; e < 16; ++e) {
     const uint64_t x = pr_fma2(pr_two(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), c2, off2);
-    float2 y;
-    if ((e & 7) < kPrFmaPairs) {
-      y = pr_exp2_fma(x);
-    } else {
-      y = pr_both(x);
-      y = make_float2(pr_ex2(y.x), pr_ex2(y.y));
-    }
+    float2 y = pr_both(x);
+    y = make_float2(pr_ex2(y.x), pr_ex2(y.y));
     ls[e & 1] = pr_add2(ls[e & 1], pr_two(y.x, y.y));
     pk[e] = tc_pack(y.x, y.y);
   }
@@ -441,120 +419,121 @@ __device__ __forceinline__ float pr_top(const uint32_t* s, int n) {
 }
 constexpr float kPrScale = 1.4426950408889634f * 0.08838834764831845f;  // log2(e) / sqrt(128)
 
-// One block of a row tile that every row sees whole: S out of tensor memory, P
-// into it, m_ref, l and O brought along. After the maximum, columns 64 .. 127
-// are still in registers and go first; 0 .. 63 are read again meanwhile. P
-// takes the place of S's columns 64 .. 127 (kPrP).
-__device__ __forceinline__ void pr_softmax_whole(PrRow& row, uint32_t t_s, uint32_t t_o, bool first, uint64_t* half,
-                                                 int lane) {
-  uint32_t a[64], b[64], pk[32];
+// The two warps of a row quadrant meet at a named barrier. A warp whose wait
+// for the tensor core gave up still comes, having raised `failed`, and both
+// leave together: neither is left at the barrier.
+struct PrPair {
+  int id;                 // barrier 1 .. 8
+  volatile int* failed;   // one word for the block
+  volatile float* mine;   // this thread's slot, the other thread's
+  volatile float* other;
+};
+__device__ __forceinline__ void pr_meet(const PrPair& pr) {
+  asm volatile("barrier.cta.sync %0, 64;" ::"r"(pr.id) : "memory");
+}
+// The larger of the two threads' values. The slots are free again once both
+// warps have handed over P, before the next S.
+__device__ __forceinline__ float pr_join(float x, const PrPair& pr, bool& ok) {
+  *pr.mine = x;
+  pr_meet(pr);
+  ok = *pr.failed == 0;
+  return pr_max(x, *pr.other);
+}
+
+// 64 columns of a block that every row sees whole: S out of tensor memory, P
+// into it, m_ref, l and this half of O brought along.
+__device__ __forceinline__ bool pr_softmax_whole(PrRow& row, uint32_t t_s, uint32_t t_o, bool first, const PrPair& pr) {
+  uint32_t a[32], b[32], pk[32];
   pr_ld32(t_s, b);
-  pr_ld32(t_s + 32, b + 32);
-  pr_ld32(t_s + 64, a);
-  pr_ld32(t_s + 96, a + 32);
+  pr_ld32(t_s + 32, a);
   pr_ld_wait(b);
-  pr_ld_wait(b + 32);
   pr_ld_wait(a);
-  pr_ld_wait(a + 32);
-  pr_follow(row, pr_max(pr_top(b, 64), pr_top(a, 64)) * kPrScale, t_o, first);
+  bool ok;
+  const float top = pr_join(pr_max(pr_top(b, 32), pr_top(a, 32)), pr, ok);
+  if (!ok) return false;
+  pr_follow(row, top * kPrScale, t_o, first);
   const float off = row.m_ref == -INFINITY ? 0.0f : -row.m_ref;
   const uint64_t c2 = pr_two(kPrScale, kPrScale), off2 = pr_two(off, off);
   uint64_t ls[2] = {0, 0};
-  pr_ld32(t_s, b);
-  pr_probs(a, pk, c2, off2, ls);
-  pr_probs(a + 32, pk + 16, c2, off2, ls);
-  pr_ld_wait(b);
-  pr_ld32(t_s + 32, b + 32);
-  pr_st16(t_s + kPrP + 32, pk);
-  pr_st16(t_s + kPrP + 48, pk + 16);
   pr_probs(b, pk, c2, off2, ls);
-  pr_ld_wait(b + 32);
-  pr_stored(half, lane);
+  pr_probs(a, pk + 16, c2, off2, ls);
   pr_st16(t_s + kPrP, pk);
-  pr_probs(b + 32, pk, c2, off2, ls);
-  pr_st16(t_s + kPrP + 16, pk);
+  pr_st16(t_s + kPrP + 16, pk + 16);
   const float2 y = pr_both(pr_add2(ls[0], ls[1]));
   row.l += y.x + y.y;
+  return true;
 }
 
-// The same for chunks [ca, cb) under the rows' masks. bad: the block's pages
-// outside the pool.
-__device__ __forceinline__ void pr_softmax_part(PrRow& row, uint32_t t_s, uint32_t t_o, int t0, int ca, int cb, bool first,
-                                           unsigned bad, int log2bs) {
-  auto on = [&](int q) { return q >= ca && q < cb; };
-  // S is read twice, for the maximum and for the exponentials: 32 columns at
-  // a time in registers, the next 32 on their way
-  uint32_t ms[4];
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    ms[q] = pr_mask(row.v, t0, q);
-    if (bad)
-      for (int e = 0; e < 32; ++e)
-        if ((bad >> min((q * 32 + e) >> log2bs, 31)) & 1u) ms[q] &= ~(1u << e);
-  }
-  auto hide = [&](uint32_t* s, int q) {
+// The same under the rows' masks, for those of the half's two 32-column
+// chunks (c0, c0 + 1) that lie in [ca, cb). bad: the block's pages outside the
+// pool.
+__device__ __forceinline__ bool pr_softmax_part(PrRow& row, uint32_t t_s, uint32_t t_o, int t0, int c0, int ca, int cb,
+                                                bool first, unsigned bad, int log2bs, const PrPair& pr) {
+  uint32_t s[32], ms[2];
+  float mx = -INFINITY;
+  auto hide = [&](int q) {
 #pragma unroll
     for (int e = 0; e < 32; ++e)
       if (!((ms[q] >> e) & 1u)) s[e] = 0xFF800000u;  // -inf
   };
-  float mx = -INFINITY;
-  uint32_t sa[32], sb[32];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    if (on(2 * h)) pr_ld32(t_s + 64 * h, sa);
-    if (on(2 * h + 1)) pr_ld32(t_s + 64 * h + 32, sb);
-    auto top = [&](uint32_t* s, int q) {
-      if (!on(q)) return;
-      pr_ld_wait(s);
-      hide(s, q);
-      mx = pr_max(mx, pr_top(s, 32));
-    };
-    top(sa, 2 * h);
-    top(sb, 2 * h + 1);
+  for (int q = 0; q < 2; ++q) {
+    const int ch = c0 + q;
+    if (ch < ca || ch >= cb) continue;
+    ms[q] = pr_mask(row.v, t0, ch);
+    if (bad)
+      for (int e = 0; e < 32; ++e)
+        if ((bad >> min((ch * 32 + e) >> log2bs, 31)) & 1u) ms[q] &= ~(1u << e);
+    pr_ld32(t_s + q * 32, s);
+    pr_ld_wait(s);
+    hide(q);
+    mx = pr_max(mx, pr_top(s, 32));
   }
-  pr_follow(row, mx * kPrScale, t_o, first);
-  // downwards: P of a chunk takes the place of columns that are read by then
-  if (on(3)) pr_ld32(t_s + 96, sa);
+  bool ok;
+  const float top = pr_join(mx, pr, ok);
+  if (!ok) return false;
+  pr_follow(row, top * kPrScale, t_o, first);
   const float off = row.m_ref == -INFINITY ? 0.0f : -row.m_ref;
   const uint64_t c2 = pr_two(kPrScale, kPrScale), off2 = pr_two(off, off);
   uint64_t ls[2] = {0, 0};
-  auto probs = [&](uint32_t* s, uint32_t* ahead, int q) {
-    if (on(q)) pr_ld_wait(s);
-    if (q > 0 && on(q - 1)) pr_ld32(t_s + (q - 1) * 32, ahead);
-    if (!on(q)) return;
-    hide(s, q);
+#pragma unroll
+  for (int q = 1; q >= 0; --q) {  // the upper chunk first: P takes its place
+    const int ch = c0 + q;
+    if (ch < ca || ch >= cb) continue;
     uint32_t pk[16];
+    pr_ld32(t_s + q * 32, s);
+    pr_ld_wait(s);
+    hide(q);
     pr_probs(s, pk, c2, off2, ls);
     pr_st16(t_s + kPrP + q * 16, pk);
-  };
-  probs(sa, sb, 3);
-  probs(sb, sa, 2);
-  probs(sa, sb, 1);
-  probs(sb, sa, 0);
-  const float2 a = pr_both(pr_add2(ls[0], ls[1]));
-  row.l += a.x + a.y;
+  }
+  const float2 y = pr_both(pr_add2(ls[0], ls[1]));
+  row.l += y.x + y.y;
+  return true;
 }
 
 template <int TERMS>
-__global__ void __launch_bounds__(pr_threads(TERMS), 1) span_prompt_kernel(const __grid_constant__ PromptParams p) {
+__global__ void __launch_bounds__(kPrThreads, 1) span_prompt_kernel(const __grid_constant__ PromptParams p) {
   using SM = PrSmem<TERMS>;
   constexpr int kStages = SM::kStages;
-  extern __shared__ __align__(16) unsigned char smem_raw[];
-  __shared__ double turns[kNFC];
-  const uint32_t raw = smem_u32(smem_raw);
-  unsigned char* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  extern __shared__ __align__(1024) unsigned char smem[];
   unsigned char* ring = smem + SM::kQ;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + SM::kBars);  // [kStages]
   uint64_t* empty = full + kStages;                                // [kStages]
   uint64_t* bar_s = empty + kStages;  // [2] S of a tile is ready
-  uint64_t* bar_h = bar_s + 2;        // [2] P of a block's columns 64 .. 127 is in tensor memory
-  uint64_t* bar_p = bar_h + 2;        // [2] all of P is
+  uint64_t* bar_p = bar_s + 2;        // [2] P is in tensor memory
   uint64_t* bar_o = bar_p + 2;        // [2] an item's O is complete
   uint64_t* bar_q = bar_o + 2;        // [2] an item's Q is staged
   uint64_t* bar_f = bar_q + 2;        // [2] an item's Q is no longer read
   uint32_t* tbase_s = reinterpret_cast<uint32_t*>(bar_f + 2);
+  volatile int* failed = reinterpret_cast<int*>(tbase_s + 1);
+  double* turns = reinterpret_cast<double*>(smem + SM::kTurns);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = p.s.group, hq = p.s.n_kv_heads * G, tt = pr_tokens(G);
+  if (smem_u32(smem) & 1023u) {  // the swizzled tiles would not be where TMA puts them
+    if (tid == 0) flag_status(FASA_ERR_CUDA);
+    return;
+  }
 
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -563,16 +542,16 @@ __global__ void __launch_bounds__(pr_threads(TERMS), 1) span_prompt_kernel(const
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar_s + i, 1);
-      mbar_init(bar_h + i, 4);
-      mbar_init(bar_p + i, 4);
+      mbar_init(bar_p + i, 8);
       mbar_init(bar_o + i, 1);
-      mbar_init(bar_q + i, TERMS == 1 ? 1 : kPrRotate * 32);
+      mbar_init(bar_q + i, TERMS == 1 ? 1 : 8);
       mbar_init(bar_f + i, 1);
     }
+    *failed = 0;
     fence_mbar_init();
   }
-  if (warp == 8) tc_alloc(tbase_s, 512);
-  if (TERMS == 2) span_stage_turns<pr_threads(TERMS)>(p.s, turns);
+  if (warp == 16) tc_alloc(tbase_s, 512);
+  if (TERMS == 2) span_stage_turns<kPrThreads>(p.s, turns);
   grid_dependency_wait();
   tc_fence_before();
   __syncthreads();
@@ -580,17 +559,20 @@ __global__ void __launch_bounds__(pr_threads(TERMS), 1) span_prompt_kernel(const
   const uint32_t tbase = *tbase_s;
   // tensor memory columns: S_A (and P_A) 0, S_B 128, O_A 256, O_B 384
 
-  if (warp < 8) {
-    // ------------------------------------------------ softmax of one tile
-    if (TERMS == 1)
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
-    else
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
-    const int sub = warp >> 2, r = tid & 127;  // row of the tile = TMEM lane
-    const int rt = r / G, rh = r % G;          // its token and head
+  if (warp < 16) {
+    // ----------------------------------- softmax: half of a tile's columns
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    const int sub = warp >> 3, half = (warp >> 2) & 1, r = tid & 127;  // row of the tile = TMEM lane
+    const int rt = r / G, rh = r - rt * G;                             // its token and head
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t t_s = tbase + sub * 128 + lanes, t_o = tbase + 256 + sub * 128 + lanes;
+    const uint32_t t_s = tbase + sub * 128 + half * 64 + lanes, t_o = tbase + 256 + sub * 128 + half * 64 + lanes;
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.s.out);
+    float* pair = reinterpret_cast<float*>(smem + SM::kPair) + sub * 256;
+    const PrPair pr{1 + sub * 4 + (warp & 3), failed, pair + half * 128 + r, pair + (half ^ 1) * 128 + r};
+    // a bounded wait; a warp that gave up goes on to the next meeting
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      if (!pr_wait(bar, parity)) *failed = 1;
+    };
     auto part_of = [&](const PrItem& w) {
       return p.part + (((int64_t)(w.b * p.s.n_kv_heads + w.g) * p.tiles_max + w.tile) * p.splits + w.split) * kPrPart;
     };
@@ -614,116 +596,155 @@ __global__ void __launch_bounds__(pr_threads(TERMS), 1) span_prompt_kernel(const
           pp[sub * 128 + r] = -INFINITY;
           pp[kPrRows + sub * 128 + r] = 0.0f;
         } else {
-          uint4* o = reinterpret_cast<uint4*>(out + out_row(w) * kD);
+          uint4* o = reinterpret_cast<uint4*>(out + out_row(w) * kD) + half * 8;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] = make_uint4(0, 0, 0, 0);
+          for (int i = 0; i < 8; ++i) o[i] = make_uint4(0, 0, 0, 0);
         }
       }
+    };
+    // An item's Q rows of this tile, rotated, as two bf16 terms: 8 lanes take a
+    // token, each the chunks ch and ch + 8 (dims i and i + 64 of 8 FCs), so
+    // that an angle serves the G heads. Rows past the item's are left: what S
+    // holds there is masked.
+    auto stage_q = [&](const PrItem& w) {
+      unsigned char* qs = smem + sub * TERMS * kPrTile;
+      const int ch = lane & 7, n_t = min(tt, w.n_tok - sub * tt);
+      const __nv_bfloat16* base = static_cast<const __nv_bfloat16*>(p.s.q) +
+                                  (((int64_t)w.b * p.s.n_q + w.j0 + sub * tt) * hq + w.g * G) * kD;
+      for (int jt = (warp & 7) * 4 + (lane >> 3); jt < n_t; jt += 32) {
+        float cs[8], sn[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) span_angle(turns[ch * 8 + e], w.pos0 + w.j0 + sub * tt + jt, cs + e, sn + e);
+        const uint4* src = reinterpret_cast<const uint4*>(base + (int64_t)jt * hq * kD);
+#pragma unroll 2
+        for (int h = 0; h < G; ++h) {
+          const int rr = jt * G + h;
+          float x[8], y[8], t8[8];
+          unpack16(__ldg(src + h * 16 + ch), x, __nv_bfloat16());
+          unpack16(__ldg(src + h * 16 + ch + 8), y, __nv_bfloat16());
+          uint4 hi, lo;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) t8[e] = x[e] * cs[e] - y[e] * sn[e];
+          tc_split8(t8, hi, lo);
+          *reinterpret_cast<uint4*>(qs + tc_sw(rr, ch, 128)) = hi;
+          *reinterpret_cast<uint4*>(qs + kPrTile + tc_sw(rr, ch, 128)) = lo;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) t8[e] = y[e] * cs[e] + x[e] * sn[e];
+          tc_split8(t8, hi, lo);
+          *reinterpret_cast<uint4*>(qs + tc_sw(rr, ch + 8, 128)) = hi;
+          *reinterpret_cast<uint4*>(qs + kPrTile + tc_sw(rr, ch + 8, 128)) = lo;
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) pr_arrive(bar_q + sub);
     };
     uint32_t n_s = 0, n_o = 0;  // barrier phases used
     int it = 0;
     PrItem w;
     bool more = next(it, w), ok = true;
+    if (TERMS == 2 && more && sub * tt < w.n_tok) stage_q(w);
     const int n_pg = p.s.pm.table ? max(1, kPrBlock >> p.s.pm.log2bs) : 0;
     while (more && ok) {
-      const bool mine = has_row(w);
-      if (sub * tt < w.n_tok) {
-        PrRow row;
-        row.m_ref = -INFINITY;
-        row.l = 0.0f;
+      const bool mine = has_row(w), active = sub * tt < w.n_tok;
+      PrRow row;
+      row.m_ref = -INFINITY;
+      row.l = 0.0f;
+      if (active) {
         row.v = span_of(w.L, mine ? w.pos0 + w.j0 + sub * tt + rt : -1, p.s.window, p.s.n_sink);
+        // blocks [f0, f1) are whole to every row of the tile
+        const int64_t pa = w.pos0 + w.j0 + sub * tt;
+        const Span first = span_of(w.L, pa, p.s.window, p.s.n_sink);
+        const Span last = span_of(w.L, pa + min(tt, w.n_tok - sub * tt) - 1, p.s.window, p.s.n_sink);
+        const int f0 = w.u.na + max(0, (last.lo + kPrBlock - 1) / kPrBlock - w.u.first);
+        const int f1 = w.u.na + first.hi / kPrBlock - w.u.first;
         for (int i = w.i0; i < w.i1; ++i) {
-          const int t0 = w.u.unit(i) * kPrBlock;
           unsigned bad = 0;  // the block's pages outside the pool
           if (n_pg) {
-            const int t = t0 + (lane << p.s.pm.log2bs);
+            const int t = w.u.unit(i) * kPrBlock + (lane << p.s.pm.log2bs);
             bad = __ballot_sync(0xFFFFFFFFu,
                                 lane < n_pg && t < w.all.hi &&
                                     (unsigned)__ldg(p.s.pm.table + (int64_t)w.b * p.s.pm.max_blocks +
                                                     (t >> p.s.pm.log2bs)) >= (unsigned)p.s.pm.n_pages);
           }
-          int ca, cb;
-          pr_chunks(w.all, t0, ca, cb);
-          if (!pr_wait(bar_s + sub, n_s & 1)) {
-            ok = false;
-            break;
-          }
-          ++n_s;
+          wait(bar_s + sub, n_s++ & 1);
           tc_fence_after();
-          const bool whole = t0 + kPrBlock <= row.v.hi && (t0 >= row.v.lo || t0 + kPrBlock <= row.v.s);
-          if (cb - ca == 4 && !bad && __all_sync(0xFFFFFFFFu, whole || !mine)) {
-            pr_softmax_whole(row, t_s, t_o, i == w.i0, bar_h + sub, lane);
+          if (i >= f0 && i < f1 && !bad) {
+            ok = pr_softmax_whole(row, t_s, t_o, i == w.i0, pr);
           } else {
-            pr_softmax_part(row, t_s, t_o, t0, ca, cb, i == w.i0, bad, p.s.pm.log2bs);
-            pr_stored(bar_h + sub, lane);
+            const int t0 = w.u.unit(i) * kPrBlock;
+            int ca, cb;
+            pr_chunks(w.all, t0, ca, cb);
+            ok = pr_softmax_part(row, t_s, t_o, t0, half * 2, ca, cb, i == w.i0, bad, p.s.pm.log2bs, pr);
           }
+          if (!ok) break;
           pr_stored(bar_p + sub, lane);
         }
         if (!ok) break;
-        const int64_t at = mine ? out_row(w) : -1;
-        float* pp = p.splits > 1 ? part_of(w) : nullptr;
-        ++it;
-        more = next(it, w);
-        if (!pr_wait(bar_o + sub, n_o & 1)) {
-          ok = false;
-          break;
-        }
-        ++n_o;
-        tc_fence_after();
-        if (p.splits == 1) {
-          // rows of the lane's group of four: lane k stores the k-th 16 bytes
-          // of each 64, so that a group's store covers 64 bytes of a row
-          int64_t at4[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) at4[k] = __shfl_sync(0xFFFFFFFFu, at, (lane & ~3) + k);
-          const float inv = row.l == 0.0f ? 0.0f : 1.0f / row.l;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t o[32], z[16];
-            pr_ld32(t_o + q * 32, o);
-            pr_ld_wait(o);
-#pragma unroll
-            for (int d = 0; d < 16; ++d) {
-              const float x0 = __uint_as_float(o[2 * d]) * inv, x1 = __uint_as_float(o[2 * d + 1]) * inv;
-              z[d] = row.l == 0.0f ? 0u : tc_pack(x0, x1);
-            }
-            pr_transpose4(z, lane);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (at4[k] >= 0)
-                reinterpret_cast<uint4*>(out + at4[k] * kD)[q * 4 + (lane & 3)] =
-                    make_uint4(z[4 * k], z[4 * k + 1], z[4 * k + 2], z[4 * k + 3]);
-          }
-        } else {
-          const int rr = sub * 128 + r;
-          if (mine) {
-            pp[rr] = row.m_ref;
-            pp[kPrRows + rr] = row.l;
-          }
-          uint4* po = reinterpret_cast<uint4*>(pp + 2 * kPrRows + (int64_t)rr * kD);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t o[32];
-            pr_ld32(t_o + q * 32, o);
-            pr_ld_wait(o);
-            if (mine) {
-#pragma unroll
-              for (int e = 0; e < 8; ++e) po[q * 8 + e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-            }
-          }
-        }
-        tc_fence_before();
-      } else {
-        ++it;
-        more = next(it, w);
       }
+      const int64_t at = mine ? out_row(w) : -1;
+      float* pp = p.splits > 1 ? part_of(w) : nullptr;
+      ++it;
+      more = next(it, w);
+      if (TERMS == 2 && more && sub * tt < w.n_tok) stage_q(w);  // the last S is done with the old ones
+      if (!active) continue;
+      wait(bar_o + sub, n_o++ & 1);
+      tc_fence_after();
+      // the row's sum, once both threads are past their last exchange
+      *pr.mine = row.l;
+      pr_meet(pr);
+      const float l = row.l + *pr.other;
+      ok = *failed == 0;
+      pr_meet(pr);
+      if (!ok) break;
+      if (p.splits == 1) {
+        // rows of the lane's group of four: lane k stores the k-th 16 bytes
+        // of each 64, so that a group's store covers 64 bytes of a row
+        int64_t at4[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) at4[k] = __shfl_sync(0xFFFFFFFFu, at, (lane & ~3) + k);
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t o[32], z[16];
+          pr_ld32(t_o + q * 32, o);
+          pr_ld_wait(o);
+#pragma unroll
+          for (int d = 0; d < 16; ++d) {
+            const float x0 = __uint_as_float(o[2 * d]) * inv, x1 = __uint_as_float(o[2 * d + 1]) * inv;
+            z[d] = l == 0.0f ? 0u : tc_pack(x0, x1);
+          }
+          pr_transpose4(z, lane);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (at4[k] >= 0)
+              reinterpret_cast<uint4*>(out + at4[k] * kD)[half * 8 + q * 4 + (lane & 3)] =
+                  make_uint4(z[4 * k], z[4 * k + 1], z[4 * k + 2], z[4 * k + 3]);
+        }
+      } else {
+        const int rr = sub * 128 + r;
+        if (mine && half == 0) {
+          pp[rr] = row.m_ref;
+          pp[kPrRows + rr] = l;
+        }
+        uint4* po = reinterpret_cast<uint4*>(pp + 2 * kPrRows + (int64_t)rr * kD) + half * 16;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t o[32];
+          pr_ld32(t_o + q * 32, o);
+          pr_ld_wait(o);
+          if (mine) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) po[q * 8 + e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          }
+        }
+      }
+      tc_fence_before();
     }
-  } else if (TERMS == 1) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
   }
-  if (warp == 8) {
+  if (warp == 16) {
     // ----------------------------------------------------- the products
     uint32_t kv = 0, n_p[2] = {0, 0}, n_q[2] = {0, 0};
     bool ok = true;
@@ -789,24 +810,15 @@ __global__ void __launch_bounds__(pr_threads(TERMS), 1) span_prompt_kernel(const
         for (int sub = 0; sub < subs && ok; ++sub) {
           const uint32_t d = pr_uni(tb + 256 + sub * 128), pa = pr_uni(tb + sub * 128 + kPrP),
                          v = pr_uni(v_lo + vs_st * (kPrTile >> 4));
-          if (!(ok = pr_wait(bar_h + sub, n_p[sub] & 1))) break;
-          tc_fence_after();
-          if (cb - ca == 4) {  // the upper half while the lower is still computed
-            if (pr_elect()) {
-              if (i > w.i0)
-                pr_issue_o<true>(d, pa, v, 4);
-              else
-                pr_issue_o<false>(d, pa, v, 4);
-            }
-            __syncwarp();
-          }
           if (!(ok = pr_wait(bar_p + sub, n_p[sub]++ & 1))) break;
           tc_fence_after();
           if (pr_elect()) {
-            if (cb - ca == 4)
-              pr_issue_o<true>(d, pa, v, 0);
-            else
+            if (cb - ca < 4)
               pr_issue_part(d, pa, v, ca, cb, i > w.i0);
+            else if (i > w.i0)
+              pr_issue_o<true>(d, pa, v);
+            else
+              pr_issue_o<false>(d, pa, v);
             if (last) tc_commit(bar_o + sub);
             if (sub == subs - 1) tc_commit(empty + vs_st);
           }
@@ -820,7 +832,7 @@ __global__ void __launch_bounds__(pr_threads(TERMS), 1) span_prompt_kernel(const
         cb = nb;
       }
     }
-  } else if (warp == 9) {
+  } else if (warp == 17) {
     // ------------------------------------------------------- the loads
     uint32_t n = 0, n_f[2] = {0, 0};
     bool ok = true;
@@ -884,61 +896,10 @@ __global__ void __launch_bounds__(pr_threads(TERMS), 1) span_prompt_kernel(const
     if (TERMS == 1)
       for (int sub = 0; sub < 2; ++sub)
         if (n_f[sub] > 0) mbar_wait(bar_q + sub, (n_f[sub] - 1) & 1);
-  } else if (TERMS == 2 && warp >= 16 - kPrRotate) {
-    // ---------------------------------------------- rotated queries, two terms
-    uint32_t n_f[2] = {0, 0};
-    bool ok = true;
-    PrSeq sq;
-    sq.b = -1;
-    const __nv_bfloat16* qg = static_cast<const __nv_bfloat16*>(p.s.q);
-    const int ch = lane & 7;  // 8 lanes a token, each the chunks ch and ch + 8 (dims i and i + 64 of 8 FCs)
-    for (int it = 0; ok; ++it) {
-      const PrItem w = pr_item(p, it, sq);
-      if (w.b < 0) break;
-      if (!w.valid || w.i0 >= w.i1) continue;
-      for (int sub = 0; sub < 2 && sub * tt < w.n_tok; ++sub) {
-        unsigned char* qs = smem + sub * TERMS * kPrTile;
-        const int wq = warp - (16 - kPrRotate), n_t = min(tt, w.n_tok - sub * tt);
-        const __nv_bfloat16* base = qg + (((int64_t)w.b * p.s.n_q + w.j0 + sub * tt) * hq + w.g * G) * kD;
-        for (int e = wq * 32 + lane; e < n_t * 2 * G; e += kPrRotate * 32)  // on their way to L2 meanwhile
-          prefetch_line_l2(base + (int64_t)(e / (2 * G)) * hq * kD + (e % (2 * G)) * 64);
-        if (n_f[sub] > 0 && !pr_wait(bar_f + sub, (n_f[sub] - 1) & 1)) {
-          ok = false;
-          break;
-        }
-        ++n_f[sub];
-        for (int jt = wq * 4 + (lane >> 3); jt < n_t; jt += 4 * kPrRotate) {
-          float cs[8], sn[8];  // an angle serves the G heads
-#pragma unroll
-          for (int e = 0; e < 8; ++e) span_angle(turns[ch * 8 + e], w.pos0 + w.j0 + sub * tt + jt, cs + e, sn + e);
-          const uint4* src = reinterpret_cast<const uint4*>(base + (int64_t)jt * hq * kD);
-#pragma unroll 2
-          for (int h = 0; h < G; ++h) {
-            const int rr = jt * G + h;
-            float x[8], y[8], t8[8];
-            unpack16(__ldg(src + h * 16 + ch), x, __nv_bfloat16());
-            unpack16(__ldg(src + h * 16 + ch + 8), y, __nv_bfloat16());
-            uint4 hi, lo;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) t8[e] = x[e] * cs[e] - y[e] * sn[e];
-            tc_split8(t8, hi, lo);
-            *reinterpret_cast<uint4*>(qs + tc_sw(rr, ch, 128)) = hi;
-            *reinterpret_cast<uint4*>(qs + kPrTile + tc_sw(rr, ch, 128)) = lo;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) t8[e] = y[e] * cs[e] + x[e] * sn[e];
-            tc_split8(t8, hi, lo);
-            *reinterpret_cast<uint4*>(qs + tc_sw(rr, ch + 8, 128)) = hi;
-            *reinterpret_cast<uint4*>(qs + kPrTile + tc_sw(rr, ch + 8, 128)) = lo;
-          }
-        }
-        fence_proxy_async_smem();
-        pr_arrive(bar_q + sub);
-      }
-    }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) tc_dealloc(tbase, 512);
+  if (warp == 16) tc_dealloc(tbase, 512);
   grid_dependents_launch();
 }
 
