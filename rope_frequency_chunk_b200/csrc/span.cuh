@@ -170,35 +170,57 @@ struct SpanWhere {
   int b, units;
 };
 __device__ __forceinline__ int span_cost(int units) { return units > 0 ? units + kSpanSetup : 0; }
-template <int NT>
-__device__ __forceinline__ int64_t span_total(const SpanParams& p, int64_t* sm) {
-  int64_t t = 0;
-  for (int b = threadIdx.x; b < p.batch; b += NT) t += span_cost(span_seq_units(p, b));
-  int64_t before;
-  return span_scan<NT>(t, sm, before) * p.n_kv_heads;
-}
-// Block-wide: finds sequence `at`, or the one that holds cost u (at < 0); b =
-// -1 when none does. `out` is shared memory.
-template <int NT>
-__device__ __forceinline__ void span_find(const SpanParams& p, int at, int64_t u, int64_t* sm, SpanWhere* out) {
-  if (threadIdx.x == 0) out->b = -1;
-  int64_t run = 0;
-  for (int b0 = 0; b0 < p.batch; b0 += NT) {
-    const int b = b0 + threadIdx.x;
-    const int n = b < p.batch ? span_seq_units(p, b) : 0;
-    int64_t before;
-    const int64_t cost = (int64_t)span_cost(n) * p.n_kv_heads;
-    const int64_t sum = span_scan<NT>(cost, sm, before);
-    before += run;
-    const bool mine = at >= 0 ? b == at : (n > 0 && before <= u && u < before + cost);
-    if (mine) {
-      out->b = b;
-      out->base = before;
-      out->units = n;
-    }
-    run += sum;
+
+// The sequences' costs, summed up once per block: thread i's are sequences
+// [i q, (i + 1) q), q = ceil(B / 128), and cum[i] is the cost ahead of them.
+struct SpanIndex {
+  int64_t cum[kSpanThreads + 1];
+  int units[kSpanThreads];  // of sequence i, where q is 1
+  int64_t scan[kSpanWarps];
+};
+__device__ __forceinline__ int64_t span_index(const SpanParams& p, SpanIndex& x) {  // returns the total
+  const int tid = threadIdx.x, q = (p.batch + kSpanThreads - 1) / kSpanThreads;
+  int64_t mine = 0;
+  for (int b = tid * q; b < min((tid + 1) * q, p.batch); ++b) {
+    const int n = span_seq_units(p, b);
+    mine += (int64_t)span_cost(n) * p.n_kv_heads;
+    if (q == 1) x.units[tid] = n;
   }
+  int64_t before;
+  const int64_t total = span_scan<kSpanThreads>(mine, x.scan, before);
+  x.cum[tid] = before;
+  if (tid == 0) x.cum[kSpanThreads] = total;
   __syncthreads();
+  return total;
+}
+__device__ __forceinline__ int span_units_of(const SpanParams& p, const SpanIndex& x, int b) {
+  return p.batch <= kSpanThreads ? x.units[b] : span_seq_units(p, b);
+}
+// Sequence b, and the sequence that holds cost u < total (a whole warp asks).
+__device__ __forceinline__ SpanWhere span_at(const SpanParams& p, const SpanIndex& x, int b) {
+  const int q = (p.batch + kSpanThreads - 1) / kSpanThreads;
+  SpanWhere w;
+  w.b = b / q * q;
+  w.base = x.cum[b / q];
+  for (w.units = span_units_of(p, x, w.b); w.b < b; w.units = span_units_of(p, x, ++w.b))
+    w.base += (int64_t)span_cost(w.units) * p.n_kv_heads;
+  return w;
+}
+__device__ __forceinline__ SpanWhere span_find(const SpanParams& p, const SpanIndex& x, int64_t u) {
+  const int q = (p.batch + kSpanThreads - 1) / kSpanThreads, lane = threadIdx.x & 31;
+  int n = 0;  // groups that begin at or before u: the last of them holds it (empty ones are ahead of it)
+#pragma unroll
+  for (int k = 0; k < kSpanThreads / 32; ++k) n += __popc(__ballot_sync(0xFFFFFFFFu, x.cum[k * 32 + lane] <= u));
+  // groups behind the last sequence begin at the total, beyond u
+  SpanWhere w;
+  w.b = (n - 1) * q;
+  w.base = x.cum[n - 1];
+  for (;; ++w.b) {
+    w.units = span_units_of(p, x, w.b);
+    const int64_t cost = (int64_t)span_cost(w.units) * p.n_kv_heads;
+    if (u < w.base + cost || w.b + 1 >= p.batch) return w;
+    w.base += cost;
+  }
 }
 
 // ------------------------------------------------------- rows seen by no one
@@ -267,8 +289,7 @@ struct alignas(16) SpanCcSmem {
   float m[kSpanWarps][MG], l[kSpanWarps][MG];
   float o[kSpanWarps][MG][kD];
   double turns[kNFC];
-  int64_t scan[kSpanWarps];
-  SpanWhere where;
+  SpanIndex index;
 };
 
 // The rotation table into shared memory. Indexed per thread, the kernel
@@ -510,17 +531,16 @@ __global__ void __launch_bounds__(kSpanThreads) span_cc_kernel(const __grid_cons
     return;
   }
   span_zero_rows<T, kSpanThreads>(p);
-  const int64_t total = span_total<kSpanThreads>(p, sm.scan);
+  const int64_t total = span_index(p, sm.index);
   const int n_cta = span_ctas(total, p.n_cta);
   if ((int)blockIdx.x >= n_cta) return;
   int64_t u0 = span_cut(total, blockIdx.x, n_cta);
   const int64_t u1 = span_cut(total, blockIdx.x + 1, n_cta);
-  span_find<kSpanThreads>(p, -1, u0, sm.scan, &sm.where);
-  int b = sm.where.b;
-  if (b < 0) return;
-  const int64_t at = u0 - sm.where.base;
-  int g = (int)(at / span_cost(sm.where.units));
-  int a0 = (int)(at % span_cost(sm.where.units));  // cost within the row
+  const SpanWhere where = span_find(p, sm.index, u0);
+  int b = where.b;
+  const int64_t at = u0 - where.base;
+  int g = (int)(at / span_cost(where.units));
+  int a0 = (int)(at % span_cost(where.units));  // cost within the row
   for (bool first = true; u0 < u1;) {
     const int L = span_len(p, b);
     const int64_t pos = span_pos0(p, b, L, 1);
@@ -585,28 +605,28 @@ __device__ __forceinline__ SpanShare span_share(const SpanParams& p, int64_t tot
 template <typename T>
 __global__ void __launch_bounds__(kSpanThreads) span_join_kernel(const __grid_constant__ SpanJoinParams jp) {
   const SpanParams& p = jp.s;
-  __shared__ int64_t scan[kSpanWarps];
-  __shared__ SpanWhere where, wheres[kSpanWarps];
+  __shared__ SpanIndex index;
   __shared__ float s_l[kSpanWarps];
   __shared__ __align__(16) float s_o[kSpanWarps][kD];
   grid_dependency_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int G = p.group;
-  const int64_t total = span_total<kSpanThreads>(p, scan);
+  const int64_t total = span_index(p, index);
 
   if ((int)blockIdx.x >= jp.n_mass) {
     const int e = blockIdx.x - jp.n_mass, h = e % G, x = e / G;
     int64_t row, row_base;
+    SpanWhere where;
     if (jp.by_row) {
       row = x;
-      span_find<kSpanThreads>(p, x / p.n_kv_heads, 0, scan, &where);
+      where = span_at(p, index, x / p.n_kv_heads);
       if (where.units == 0) return;
       row_base = where.base + (int64_t)(x % p.n_kv_heads) * span_cost(where.units);
     } else {
       const int n_cta = span_ctas(total, p.n_cta), c = x + 1;
       if (c >= n_cta) return;
       const int64_t cut = span_cut(total, c, n_cta);
-      span_find<kSpanThreads>(p, -1, cut, scan, &where);
+      where = span_find(p, index, cut);
       const int64_t g = (cut - where.base) / span_cost(where.units);
       row = (int64_t)where.b * p.n_kv_heads + g;
       row_base = where.base + g * span_cost(where.units);
@@ -650,18 +670,13 @@ __global__ void __launch_bounds__(kSpanThreads) span_join_kernel(const __grid_co
   // the weights of this warp's run
   const int n_run = jp.n_mass * kSpanWarps, run = blockIdx.x * kSpanWarps + warp;
   if (total == 0) return;
-  // the sequences of the four warps' first costs, one block-wide search each
-#pragma unroll 1
-  for (int w = 0; w < kSpanWarps; ++w) {
-    const int64_t u = span_cut(total, blockIdx.x * kSpanWarps + w, n_run);
-    span_find<kSpanThreads>(p, -1, min(u, total - 1), scan, &wheres[w]);
-  }
   int64_t u0 = span_cut(total, run, n_run);
   const int64_t u1 = span_cut(total, run + 1, n_run);
   if (u0 >= u1) return;
-  int b = wheres[warp].b;
-  const int64_t at = u0 - wheres[warp].base;
-  const int cost0 = span_cost(wheres[warp].units);
+  const SpanWhere where = span_find(p, index, u0);
+  int b = where.b;
+  const int64_t at = u0 - where.base;
+  const int cost0 = span_cost(where.units);
   int g = (int)(at / cost0), a0 = (int)(at % cost0);
   int64_t row_base = u0 - a0;
   const bool vec = p.mass_ld % 4 == 0 && (reinterpret_cast<uintptr_t>(p.mass) & 15) == 0;
@@ -688,22 +703,23 @@ __global__ void __launch_bounds__(kSpanThreads) span_join_kernel(const __grid_co
           r_h = __ldcg(p.rstat + row * 2 * G + G + lane);
         }
       } else {
-        for (int h = 0; h < G; ++h) {
-          float M = -INFINITY;
-          for (int c = sh.c0 + lane; c <= sh.c1; c += 32) M = fmaxf(M, __ldcg(sh.part(p, c) + h));
-#pragma unroll
-          for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
-          float S = 0.0f;
-          for (int c = sh.c0 + lane; c <= sh.c1; c += 32) {
-            const float mc = __ldcg(sh.part(p, c) + h);
-            S += mc == -INFINITY ? 0.0f : exp2f(mc - M) * __ldcg(sh.part(p, c) + 16 + h);
-          }
-#pragma unroll
-          for (int o = 16; o; o >>= 1) S += __shfl_xor_sync(0xFFFFFFFFu, S, o);
-          if (lane == h) {
-            m_h = M;
-            r_h = S;
-          }
+        // 32 / gp partials of all heads at a time; the lanes of a head join theirs
+        const int gp = G <= 1 ? 1 : G <= 2 ? 2 : G <= 4 ? 4 : G <= 8 ? 8 : 16;
+        const int h = lane & (gp - 1);
+        for (int c = sh.c0 + lane / gp; c <= sh.c1; c += 32 / gp) {
+          if (h >= G) break;
+          const float* pp = sh.part(p, c);
+          const float m2 = __ldcg(pp + h), l2 = __ldcg(pp + 16 + h);
+          const float M = fmaxf(m_h, m2);
+          if (M == -INFINITY) continue;
+          r_h = r_h * exp2f(m_h - M) + l2 * exp2f(m2 - M);
+          m_h = M;
+        }
+        for (int o = gp; o < 32; o <<= 1) {
+          const float m2 = __shfl_xor_sync(0xFFFFFFFFu, m_h, o), l2 = __shfl_xor_sync(0xFFFFFFFFu, r_h, o);
+          const float M = fmaxf(m_h, m2);
+          if (M != -INFINITY) r_h = r_h * exp2f(m_h - M) + l2 * exp2f(m2 - M);
+          m_h = M;
         }
       }
       r_h = r_h == 0.0f ? 0.0f : 1.0f / r_h;

@@ -224,8 +224,7 @@ __global__ void __launch_bounds__(kSpanThreads, 2) span_decode_kernel(const __gr
   constexpr int kH = GT / 8;
   const SpanParams& p = pp.s;
   extern __shared__ __align__(16) unsigned char smem_raw[];
-  __shared__ int64_t scan[kSpanWarps];
-  __shared__ SpanWhere where;
+  __shared__ SpanIndex index;
   const uint32_t raw = smem_u32(smem_raw);
   unsigned char* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -242,6 +241,10 @@ __global__ void __launch_bounds__(kSpanThreads, 2) span_decode_kernel(const __gr
     fence_mbar_init();
   }
   __syncwarp();
+  if (tid == 0) {
+    prefetch_tensor_map(&pp.map_k);
+    prefetch_tensor_map(&pp.map_v);
+  }
   span_stage_turns<kSpanThreads>(p, turns);
   grid_dependency_wait();
 
@@ -260,11 +263,11 @@ __global__ void __launch_bounds__(kSpanThreads, 2) span_decode_kernel(const __gr
     }
   } else {
     span_zero_rows<__nv_bfloat16, kSpanThreads>(p);
-    const int64_t total = span_total<kSpanThreads>(p, scan);
+    const int64_t total = span_index(p, index);
     const int n_cta = span_ctas(total, p.n_cta);
     if ((int)blockIdx.x >= n_cta) return;
     const int64_t u0 = span_cut(total, blockIdx.x, n_cta);
-    span_find<kSpanThreads>(p, -1, u0, scan, &where);
+    const SpanWhere where = span_find(p, index, u0);
     use.b = where.b;
     const int64_t at = u0 - where.base;
     use.g = (int)(at / span_cost(where.units));

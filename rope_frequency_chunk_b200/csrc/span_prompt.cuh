@@ -551,6 +551,11 @@ __global__ void __launch_bounds__(kPrThreads, 1) span_prompt_kernel(const __grid
     fence_mbar_init();
   }
   if (warp == 16) tc_alloc(tbase_s, 512);
+  if (tid == 544) {  // the loader
+    prefetch_tensor_map(&p.map_k);
+    prefetch_tensor_map(&p.map_v);
+    if (TERMS == 1) prefetch_tensor_map(&p.map_q);
+  }
   if (TERMS == 2) span_stage_turns<kPrThreads>(p.s, turns);
   grid_dependency_wait();
   tc_fence_before();

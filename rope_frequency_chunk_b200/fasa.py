@@ -137,8 +137,8 @@ def _check(status: int, call: str):
 
 
 def _stream(stream) -> int | None:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # the current stream's handle, without a Stream object around it
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -463,22 +463,16 @@ def fasa_decode_multi(cache: KVCache, length: int, q, q_pos0: int, k: int, out=N
 
 # ------------------------------------- spans, eviction, appends to slots
 
-class _on:
-    """Makes a tensor's device the current one for a call (the library
+def _launch(name, t, stream, *args) -> None:
+    """Calls name(*args, stream) with tensor t's device current (the library
     launches on the current device)."""
-
-    def __init__(self, t):
-        self.other = None
-        if t.device.index != torch.cuda.current_device():
-            self.other = torch.cuda.device(t.device)
-
-    def __enter__(self):
-        if self.other is not None:
-            self.other.__enter__()
-
-    def __exit__(self, *a):
-        if self.other is not None:
-            self.other.__exit__(*a)
+    dev = t.get_device()
+    if dev != torch._C._cuda_getDevice():
+        with torch.cuda.device(dev):
+            return _launch(name, t, stream, *args)
+    status = getattr(lib(), name)(*args, _stream(stream))
+    if status != 0:
+        _check(status, name)
 
 
 def _pages(cache):
@@ -510,9 +504,10 @@ def _per_slot(cache, t, name, dtype):
 def _span(cache, seq_len, max_seq_len, window, n_sink, q_pos, q_len, q_prerotated):
     if seq_len is None:
         raise TypeError("seq_len must be a CUDA tensor")
-    return fasa_span(_per_seq(cache, seq_len, "seq_len"), _per_seq(cache, q_pos, "q_pos"),
-                     _per_seq(cache, q_len, "q_len"), int(max_seq_len), int(window), int(n_sink),
-                     1 if q_prerotated else 0)
+    return fasa_span(_per_seq(cache, seq_len, "seq_len"),
+                     None if q_pos is None else _per_seq(cache, q_pos, "q_pos"),
+                     None if q_len is None else _per_seq(cache, q_len, "q_len"),
+                     int(max_seq_len), int(window), int(n_sink), 1 if q_prerotated else 0)
 
 
 def _bounds(max_seq_len, window=0, n_sink=0):
@@ -550,10 +545,8 @@ def fasa_attend_decode(cache, seq_len, q, max_seq_len: int, window: int = 0, n_s
     if workspace is None:
         workspace = fasa_attend_decode_workspace(cache, max_seq_len, mass is not None, q.device)
     _dev(workspace, "workspace", torch.uint8)
-    with _on(q):
-        _check(lib().fasa_attend_decode(cache.ref(), _pages(cache), ctypes.byref(sp), q.data_ptr(), out.data_ptr(), m,
-                                        workspace.data_ptr(), workspace.numel(), _stream(stream)),
-               "fasa_attend_decode")
+    _launch("fasa_attend_decode", q, stream, cache.ref(), _pages(cache), ctypes.byref(sp), q.data_ptr(),
+            out.data_ptr(), m, workspace.data_ptr(), workspace.numel())
     return out
 
 
@@ -586,10 +579,8 @@ def fasa_attend_prompt(cache, seq_len, q, max_seq_len: int, window: int = 0, n_s
     if workspace is None:
         workspace = fasa_attend_prompt_workspace(cache, n_q, max_seq_len, q.device)
     _dev(workspace, "workspace", torch.uint8)
-    with _on(q):
-        _check(lib().fasa_attend_prompt(cache.ref(), _pages(cache), ctypes.byref(sp), q.data_ptr(), n_q,
-                                        out.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream(stream)),
-               "fasa_attend_prompt")
+    _launch("fasa_attend_prompt", q, stream, cache.ref(), _pages(cache), ctypes.byref(sp), q.data_ptr(), n_q,
+            out.data_ptr(), workspace.data_ptr(), workspace.numel())
     return out
 
 
@@ -629,9 +620,8 @@ def fasa_evict(cache, seq_len, cur_pos, mass, slot_pos, max_seq_len: int, budget
     if workspace is None:
         workspace = fasa_evict_workspace(cache, max_seq_len, budget, seq_len.device)
     _dev(workspace, "workspace", torch.uint8)
-    with _on(seq_len):
-        _check(lib().fasa_evict(cache.ref(), _pages(cache), ctypes.byref(d), mp, sp, mo, so, lo,
-                                workspace.data_ptr(), workspace.numel(), _stream(stream)), "fasa_evict")
+    _launch("fasa_evict", seq_len, stream, cache.ref(), _pages(cache), ctypes.byref(d), mp, sp, mo, so, lo,
+            workspace.data_ptr(), workspace.numel())
     return len_out
 
 
@@ -648,9 +638,8 @@ def fasa_append_kv_at(cache, k_new, v_new, slot0, pos0, slot_pos=None, mass=None
         raise TypeError("slot0 and pos0 must be CUDA tensors")
     s0, p0 = _per_seq(cache, slot0, "slot0"), _per_seq(cache, pos0, "pos0")
     sp, m = _per_slot(cache, slot_pos, "slot_pos", torch.int32), _per_slot(cache, mass, "mass", torch.float32)
-    with _on(k_new):
-        _check(lib().fasa_append_kv_at(cache.ref(), _pages(cache), k_new.data_ptr(), v_new.data_ptr(), n_new, s0, p0,
-                                       sp, m, _stream(stream)), "fasa_append_kv_at")
+    _launch("fasa_append_kv_at", k_new, stream, cache.ref(), _pages(cache), k_new.data_ptr(), v_new.data_ptr(), n_new,
+            s0, p0, sp, m)
 
 
 DECODE_AUTO, DECODE_FUSED, DECODE_STAGED = 0, 1, 2
