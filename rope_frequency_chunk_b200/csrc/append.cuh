@@ -46,13 +46,20 @@ struct AppendParams {
   double theta[kNFC];    // base^(-2i/128), computed on the host in float64
 };
 
+// Two neighbouring elements of a row, one load or store.
+template <typename T>
+struct alignas(2 * sizeof(T)) Two {
+  T v[2];
+};
+
 template <typename T>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams p) {
   __shared__ double s_cos[kAppendTok][kNFC];
   __shared__ double s_sin[kAppendTok][kNFC];
-  __shared__ T s_row[kAppendTok][kD];
+  __shared__ __align__(16) T s_row[kAppendTok][kD];
   __shared__ int s_dom[kNFC];
   __shared__ int64_t s_dst[kAppendTok];  // each token's row in the K / V / sketch planes, or -1
+  __shared__ double s_theta[kNFC];
 
   const int tid = threadIdx.x;
   const int tok0 = blockIdx.x * kAppendTok;
@@ -60,17 +67,21 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
   const int row0 = blockIdx.y * p.heads_per_cta;
   const int row1 = min(p.n_rows, row0 + p.heads_per_cta);
 
+  // a copy in shared memory: indexed per thread, the kernel parameters are
+  // read one address at a time
+  if (tid < kNFC) s_theta[tid] = p.theta[tid];
+  __syncthreads();
   auto angles = [&](int pos) {
     for (int e = tid; e < ntok * kNFC; e += kAppendThreads) {
       const int t = e / kNFC, i = e % kNFC;
-      const double ang = (double)(pos + tok0 + t) * p.theta[i];
+      const double ang = (double)(pos + tok0 + t) * s_theta[i];
       double s, c;
       sincos(ang, &s, &c);
       s_cos[t][i] = c;
       s_sin[t][i] = s;
     }
   };
-  int cur = p.pos0;
+  int cur = p.pos0v ? -1 : p.pos0;  // the position that s_cos is for (-1: none yet)
   if (!p.pos0v) angles(cur);
 
   for (int row = row0; row < row1; ++row) {
@@ -84,12 +95,28 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
         if (tid == 0 && blockIdx.x == 0) flag_status(FASA_ERR_BAD_INDEX);
         continue;
       }
-      if (row == row0 || pos != cur) {
+      if (pos != cur) {
         __syncthreads();  // the previous row is done with the angles
         angles(pos);
         cur = pos;
       }
     }
+    // this row's inputs are on their way while the block gets ready: a thread
+    // takes two FCs of a token's key (dims i, i + 1, i + 64, i + 65) and
+    // 16-byte vectors of its values
+    const T* kin = static_cast<const T*>(p.k_new) + ((int64_t)row * p.n_new + tok0) * kD;
+    const T* vin = static_cast<const T*>(p.v_new) + ((int64_t)row * p.n_new + tok0) * kD;
+    constexpr int kVecRow = kD * (int)sizeof(T) / 16;  // 16-byte vectors per row
+    static_assert(kAppendTok * kNFC / 2 == kAppendThreads && kAppendTok * kVecRow <= kAppendThreads,
+                  "one pair of FCs and at most one vector per thread");
+    const int kt = tid / (kNFC / 2), ki = tid % (kNFC / 2) * 2, vt = tid / kVecRow;
+    Two<T> lo, hi;
+    uint4 val = make_uint4(0, 0, 0, 0);
+    if (kt < ntok) {
+      lo = *reinterpret_cast<const Two<T>*>(kin + kt * kD + ki);
+      hi = *reinterpret_cast<const Two<T>*>(kin + kt * kD + ki + kNFC);
+    }
+    if (vt < ntok) val = reinterpret_cast<const uint4*>(vin)[tid];
     __syncthreads();  // s_cos ready; previous row done with s_row / s_dom / s_dst
     if (tid < ntok) {
       const int t = slot + tok0 + tid;
@@ -109,8 +136,6 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
       }
       s_dom[tid] = d;
     }
-    const T* kin = static_cast<const T*>(p.k_new) + ((int64_t)row * p.n_new + tok0) * kD;
-    const T* vin = static_cast<const T*>(p.v_new) + ((int64_t)row * p.n_new + tok0) * kD;
     T* kc = static_cast<T*>(p.k);
     T* vc = static_cast<T*>(p.v);
     T* sk = static_cast<T*>(p.sketch);
@@ -118,30 +143,27 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
 
     // RoPE of FC i: (x, y) -> (x cos - y sin, y cos + x sin), float64, no
     // contraction, one rounding to the cache dtype.
-    for (int e = tid; e < ntok * kNFC; e += kAppendThreads) {
-      const int t = e / kNFC, i = e % kNFC;
-      const double x = to_float(kin[t * kD + i]);
-      const double y = to_float(kin[t * kD + i + kNFC]);
-      const double c = s_cos[t][i], s = s_sin[t][i];
-      const double xr = __dsub_rn(__dmul_rn(x, c), __dmul_rn(y, s));
-      const double yr = __dadd_rn(__dmul_rn(y, c), __dmul_rn(x, s));
-      T xs, ys;
-      round_store(&xs, xr);
-      round_store(&ys, yr);
-      const int64_t dst = s_dst[t];
-      if (dst >= 0) {
-        kc[dst * kD + i] = xs;
-        kc[dst * kD + i + kNFC] = ys;
+    if (kt < ntok) {
+      Two<T> xo, yo;
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        const double x = to_float(lo.v[f]), y = to_float(hi.v[f]);
+        const double c = s_cos[kt][ki + f], s = s_sin[kt][ki + f];
+        round_store(&xo.v[f], __dsub_rn(__dmul_rn(x, c), __dmul_rn(y, s)));
+        round_store(&yo.v[f], __dadd_rn(__dmul_rn(y, c), __dmul_rn(x, s)));
       }
-      s_row[t][i] = xs;
-      s_row[t][i + kNFC] = ys;
+      const int64_t dst = s_dst[kt];
+      if (dst >= 0) {
+        *reinterpret_cast<Two<T>*>(kc + dst * kD + ki) = xo;
+        *reinterpret_cast<Two<T>*>(kc + dst * kD + ki + kNFC) = yo;
+      }
+      *reinterpret_cast<Two<T>*>(&s_row[kt][ki]) = xo;
+      *reinterpret_cast<Two<T>*>(&s_row[kt][ki + kNFC]) = yo;
     }
-    // values are stored as given (16-byte vectors)
-    constexpr int kVecRow = kD * (int)sizeof(T) / 16;  // 16-byte vectors per row
-    for (int e = tid; e < ntok * kVecRow; e += kAppendThreads) {
-      const int64_t dst = s_dst[e / kVecRow];
-      if (dst >= 0)
-        reinterpret_cast<uint4*>(vc + dst * kD)[e % kVecRow] = reinterpret_cast<const uint4*>(vin)[e];
+    // values are stored as given
+    if (vt < ntok) {
+      const int64_t dst = s_dst[vt];
+      if (dst >= 0) reinterpret_cast<uint4*>(vc + dst * kD)[tid % kVecRow] = val;
     }
     __syncthreads();
     // sketch row: dims (dom[j], dom[j]+64) at 2j, 2j+1, zero padding

@@ -373,32 +373,48 @@ __device__ __forceinline__ void span_cc_segment(const SpanParams& p, SpanCcSmem<
   const T* vb = static_cast<const T*>(p.v);
 
   const int n_steps = (i1 - i0) * (kSpanUnit / kSpanStep);
-  for (int st = warp; st < n_steps; st += kSpanWarps) {
-    const int t0 = u.unit(i0 + st / (kSpanUnit / kSpanStep)) * kSpanUnit + (st % (kSpanUnit / kSpanStep)) * kSpanStep;
-    unsigned ok = 0;  // slots of the step that count
-    int64_t r0[kSpanStep];
+  auto slot_of = [&](int st) {
+    return u.unit(i0 + st / (kSpanUnit / kSpanStep)) * kSpanUnit + (st % (kSpanUnit / kSpanStep)) * kSpanStep;
+  };
+  // requests a step's rows; returns which of its slots count
+  auto fetch = [&](int st, float4 (&k4)[kSpanStep], float4 (&v4)[kSpanStep]) -> unsigned {
+    unsigned ok = 0;
+    if (st >= n_steps) return ok;
+    const int t0 = slot_of(st);
 #pragma unroll
     for (int r = 0; r < kSpanStep; ++r) {
       const int t = t0 + r;
-      r0[r] = 0;
-      if (v.sees(t)) {
-        const int64_t at = paged ? (int64_t)paged_row(p.pm, b, g, t) : plane + t;
-        if (at >= 0) {
-          r0[r] = at;
-          ok |= 1u << r;
-        }
+      k4[r] = v4[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (!v.sees(t)) continue;
+      const int64_t at = paged ? (int64_t)paged_row(p.pm, b, g, t) : plane + t;
+      if (at < 0) continue;
+      ok |= 1u << r;
+      k4[r] = span_load4(kb + at * kD + lane * 4);
+      v4[r] = span_load4(vb + at * kD + lane * 4);
+    }
+    return ok;
+  };
+  // the next step's rows are on their way while one is worked on, where the
+  // registers allow
+  constexpr bool kAhead = MG <= 4;
+  float4 k4[kSpanStep], v4[kSpanStep], kn[kAhead ? kSpanStep : 1], vn[kAhead ? kSpanStep : 1];
+  unsigned next_ok = 0;
+  if constexpr (kAhead) next_ok = fetch(warp, kn, vn);
+  for (int st = warp; st < n_steps; st += kSpanWarps) {
+    const int t0 = slot_of(st);
+    unsigned ok;  // slots of the step that count
+    if constexpr (kAhead) {
+      ok = next_ok;
+#pragma unroll
+      for (int r = 0; r < kSpanStep; ++r) {
+        k4[r] = kn[r];
+        v4[r] = vn[r];
       }
+      next_ok = fetch(st + kSpanWarps, kn, vn);
+    } else {
+      ok = fetch(st, k4, v4);
     }
     if (ok == 0) continue;
-    float4 k4[kSpanStep], v4[kSpanStep];
-#pragma unroll
-    for (int r = 0; r < kSpanStep; ++r) {
-      k4[r] = v4[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if ((ok >> r) & 1u) {
-        k4[r] = span_load4(kb + r0[r] * kD + lane * 4);
-        v4[r] = span_load4(vb + r0[r] * kD + lane * 4);
-      }
-    }
     float z[kVals];
 #pragma unroll
     for (int r = 0; r < kSpanStep; ++r)

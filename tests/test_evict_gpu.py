@@ -169,6 +169,19 @@ def test_append_at_refuses_ranges():
     assert torch.equal(f.cache.k.nan_to_num(9.0), before.nan_to_num(9.0))
 
 
+def test_append_behind_a_skipped_sequence():
+    """A sequence out of range comes first; the others' angles are theirs."""
+    f = S.Filled([64, 64, 64], 4, 2, BF, 16)
+    kn, vn = (S.randn(f.g, 3, 2, 3, 128).to(BF) for _ in range(2))
+    F.fasa_append_kv_at(f.cache, kn, vn, i32([-1, 0, 7]), i32([5, 0, 0]))
+    assert F.fasa_device_status(clear=True) == 7
+    ref = F.KVCache(3, 4, 2, 4, 64, BF, S.BASE, [[0, 1, 2, 3], [1, 2, 3, 4]])
+    F.fasa_append_kv(ref, kn, vn, 0)
+    for b, s0 in ((1, 0), (2, 7)):
+        assert torch.equal(f.rows(f.cache.k, b, 64)[:, s0:s0 + 3], ref.k[b, :, :3])
+        assert torch.equal(f.rows(f.cache.sketch, b, 64)[:, s0:s0 + 3], ref.sketch[b, :, :3])
+
+
 @pytest.mark.parametrize("block", [0, 16])
 def test_serving_run(block):
     """The operators as a serving loop uses them, checked step by step: a
