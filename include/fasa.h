@@ -522,7 +522,10 @@ fasa_status fasa_dense_decode(const fasa_cache* cache, int32_t len, const void* 
  * then. Each query head of KV head g attends over the slots it sees:
  *   out = sum_t softmax_t(q' . k[t] / sqrt(128)) v[t],
  * and a query that sees no slot gets zeros. What the cache holds in slots
- * that no query of the call's sequence sees is never used, whatever it is.
+ * that no query of the call's sequence sees is never used, whatever it is
+ * (table entries of pages that hold only such slots are not used either). A
+ * value that is not finite, in a slot that only some of a prompt's queries
+ * see, may reach the outputs of neighbouring ones.
  *
  *  seq_len    : device [B] int32, L of each sequence, 0 .. max_seq_len (a
  *               value outside is clamped and flagged FASA_ERR_BAD_INDEX).
@@ -569,9 +572,10 @@ size_t fasa_attend_decode_workspace_bytes(const fasa_cache* cache, const fasa_sp
  *  workspace : at least fasa_attend_decode_workspace_bytes bytes, 256-byte
  *            aligned; plain scratch (no initial value, nothing kept between
  *            calls). Calls that overlap on the GPU must not share one.
- *  Arithmetic: float32 logits, softmax statistics and sums; bf16 caches use
- *  tensor-core products with the queries and the probabilities in two bf16
- *  terms each (16 significant bits). Results do not depend on timing.
+ *  Arithmetic: float32 logits, softmax statistics and sums; bf16 caches in
+ *  device memory use tensor-core products with the queries and the
+ *  probabilities in two bf16 terms each (16 significant bits). Results do not
+ *  depend on timing.
  *  A page outside the pool is flagged FASA_ERR_BAD_INDEX and its slots are
  *  left out. Errors: as fasa_decode_varlen; f32 caches are served too.
  */
@@ -594,8 +598,13 @@ size_t fasa_attend_prompt_workspace_bytes(const fasa_cache* cache, const fasa_sp
  *            output is left as it is.
  *  workspace : at least fasa_attend_prompt_workspace_bytes bytes, 256-byte
  *            aligned, as for fasa_attend_decode.
+ *  Arithmetic: as fasa_attend_decode, but the probabilities of bf16 caches
+ *  are rounded to bf16 once (their sum is not); queries given rotated are
+ *  used as they are, queries rotated here keep 16 bits in two bf16 terms.
+ *  float32 caches, and caches in host memory, take a CUDA-core kernel, a
+ *  block per query and KV head: meant for small work.
  *  Errors: as fasa_attend_decode; n_q < 1 -> FASA_ERR_INVALID_ARG; n_q >
- *  FASA_MAX_LEN -> FASA_ERR_UNSUPPORTED.
+ *  FASA_MAX_LEN, or more than 2^30 work items -> FASA_ERR_UNSUPPORTED.
  */
 fasa_status fasa_attend_prompt(const fasa_cache* cache, const fasa_paged* pages, const fasa_span* span,
                                const void* q, int32_t n_q, void* out, void* workspace, size_t workspace_bytes,

@@ -167,6 +167,21 @@ def test_clamped_lengths_and_bad_pages_are_flagged():
     assert F.fasa_device_status(clear=True) == 7 and torch.isfinite(o).all()
 
 
+def test_pages_behind_the_window_may_be_gone():
+    """Pages that hold only unseen slots need not exist (a windowed layer frees
+    them): their entries are neither used nor flagged."""
+    for bs, L, w in ((16, 900, 200), (64, 900, 200), (256, 1500, 300)):
+        f = S.Filled([L], 8, 2, BF, bs)
+        q = (S.randn(f.g, 1, 40, 8, 128) * 1.5).to(BF)
+        a = F.fasa_attend_decode(f.cache, f.seq_len, q[:, 0].contiguous(), L, window=w, n_sink=4)
+        b = F.fasa_attend_prompt(f.cache, f.seq_len, q, L, window=w, n_sink=4)
+        last = (L - 40 - w + 1) // bs  # first page that a query's window reaches
+        f.cache.block_table[0, 1:last] = -1
+        assert torch.equal(F.fasa_attend_decode(f.cache, f.seq_len, q[:, 0].contiguous(), L, window=w, n_sink=4), a)
+        assert torch.equal(F.fasa_attend_prompt(f.cache, f.seq_len, q, L, window=w, n_sink=4), b)
+        assert F.fasa_device_status(clear=True) == 0
+
+
 def test_captured_replayed_streams_and_out_of_order_workspaces():
     f = S.Filled([1200, 333], 8, 2, BF, 16)
     q = (S.randn(f.g, 2, 8, 128) * 1.5).to(BF)
