@@ -106,6 +106,22 @@ def test_evict_flags_bad_lengths_and_pages():
     assert f.cache.k.shape == before.shape
 
 
+def test_evict_in_a_host_resident_cache():
+    f = S.Filled([300], 4, 2, BF, cap=320)
+    c = F.KVCache(1, 4, 2, 4, 320, BF, S.BASE, [[0, 1, 2, 3], [1, 2, 3, 4]], kv_on_host=True)
+    c.k.copy_(f.cache.k), c.v.copy_(f.cache.v), c.sketch.copy_(f.cache.sketch)
+    torch.cuda.synchronize()
+    m = torch.rand(1, 2, 320, generator=f.g, device=S.DEV)
+    pos = torch.arange(320, device=S.DEV).int().expand(1, 2, -1).contiguous()
+    m2, pos2 = m.clone(), pos.clone()
+    for x, a, b in ((f.cache, m, pos), (c, m2, pos2)):
+        F.fasa_evict(x, f.seq_len, i32([299]), a, b, 300, 100, n_sink=4, n_recent=20)
+    torch.cuda.synchronize()
+    assert torch.equal(m, m2) and torch.equal(pos, pos2)
+    for x, y in ((f.cache.k, c.k), (f.cache.v, c.v), (f.cache.sketch, c.sketch)):
+        assert torch.equal(x[:, :, :100].cpu(), y[:, :, :100].cpu())
+
+
 def test_evict_captured_and_replayed():
     f = S.Filled([700, 600], 4, 2, BF, 16)
     c = f.cache
