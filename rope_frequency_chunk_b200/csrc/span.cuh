@@ -155,13 +155,27 @@ __device__ __forceinline__ int64_t span_scan(int64_t x, int64_t* sm, int64_t& be
 __device__ __forceinline__ int span_ctas(int64_t total, int n_cta) {
   return (int)min((int64_t)n_cta, total / (kSpanSetup + 1));
 }
-__device__ __forceinline__ int64_t span_cut(int64_t total, int c, int n_cta) { return total * c / n_cta; }
-// The CTA that owns cost u.
-__device__ __forceinline__ int span_owner(int64_t total, int64_t u, int n_cta) {
-  int c = (int)((u * n_cta) / total);
-  while (span_cut(total, c + 1, n_cta) <= u) ++c;
-  while (span_cut(total, c, n_cta) > u) --c;
-  return c;
+// n equal runs of a total: run c is [cut(c), cut(c + 1)). One 64-bit division
+// for all cuts: total = q n + r, so total c / n = c q + c r / n (n < 2^16).
+struct SpanDeal {
+  int64_t q;
+  unsigned r, n;
+  float inv;  // n / total
+  __device__ __forceinline__ int64_t cut(int c) const { return c * q + (unsigned)c * r / n; }
+  __device__ __forceinline__ int owner(int64_t u) const {  // the run that holds u
+    int c = min((int)((float)u * inv), (int)n - 1);
+    while (cut(c + 1) <= u) ++c;
+    while (cut(c) > u) --c;
+    return c;
+  }
+};
+__device__ __forceinline__ SpanDeal span_deal(int64_t total, int n) {
+  SpanDeal d;
+  d.n = (unsigned)max(n, 1);
+  d.q = total / d.n;
+  d.r = (unsigned)(total - d.q * d.n);
+  d.inv = (float)d.n / (float)max(total, (int64_t)1);
+  return d;
 }
 // A sequence's place: its index, the first cost of its KV head 0, the units
 // of one of its rows.
@@ -550,8 +564,9 @@ __global__ void __launch_bounds__(kSpanThreads) span_cc_kernel(const __grid_cons
   const int64_t total = span_index(p, sm.index);
   const int n_cta = span_ctas(total, p.n_cta);
   if ((int)blockIdx.x >= n_cta) return;
-  int64_t u0 = span_cut(total, blockIdx.x, n_cta);
-  const int64_t u1 = span_cut(total, blockIdx.x + 1, n_cta);
+  const SpanDeal deal = span_deal(total, n_cta);
+  int64_t u0 = deal.cut(blockIdx.x);
+  const int64_t u1 = deal.cut(blockIdx.x + 1);
   const SpanWhere where = span_find(p, sm.index, u0);
   int b = where.b;
   const int64_t at = u0 - where.base;
@@ -587,9 +602,9 @@ __global__ void __launch_bounds__(kSpanThreads) span_cc_kernel(const __grid_cons
 // attention's, a run per warp):
 //   mass[t] += sum_h 2^(z_ht - M_h) / L_h,
 // each lane four slots, a float4 per head. The others join rows that several
-// CTAs shared, one head each: by row where there are fewer rows than CTAs
-// (by_row), else by the cuts between the runs, cut c joining the row whose
-// first unit belongs to CTA c - 1.
+// CTAs shared: where there are fewer rows than CTAs (by_row) a CTA per row and
+// head, a row having many partials; else a CTA per cut between the runs, cut c
+// joining the row whose first unit belongs to CTA c - 1.
 struct SpanJoinParams {
   SpanParams s;
   int32_t n_mass;
@@ -604,18 +619,43 @@ struct SpanShare {
     return p.part + (int64_t)(2 * c + (c > c0 || opens ? 0 : 1)) * (kSpanHead + p.group * kD);
   }
 };
-__device__ __forceinline__ SpanShare span_share(const SpanParams& p, int64_t total, int64_t row_base, int units) {
+__device__ __forceinline__ SpanShare span_share(const SpanParams& p, const SpanDeal& d, int64_t row_base, int units) {
   SpanShare w;
-  const int n_cta = span_ctas(total, p.n_cta);
-  if (n_cta == 0) {  // one CTA per row
+  if (p.n_cta == 0) {  // one CTA per row
     w.c0 = w.c1 = 0;
     w.opens = true;
     return w;
   }
-  w.c0 = span_owner(total, row_base + kSpanSetup, n_cta);
-  w.c1 = span_owner(total, row_base + kSpanSetup + units - 1, n_cta);
-  w.opens = span_cut(total, w.c0, n_cta) >= row_base;
+  w.c0 = d.owner(row_base + kSpanSetup);
+  w.c1 = d.owner(row_base + kSpanSetup + units - 1);
+  w.opens = d.cut(w.c0) >= row_base;
   return w;
+}
+
+// A warp's sum of head h over partials first, first + step, ...: 2^(m_c - M)
+// o_c (four dims per lane) and 2^(m_c - M) l_c, M the maximum over all of the
+// row's.
+__device__ __forceinline__ float4 span_join(const SpanParams& p, const SpanShare& sh, int h, int first, int step,
+                                            int lane, float& L) {
+  float M = -INFINITY;
+  for (int c = sh.c0 + lane; c <= sh.c1; c += 32) M = fmaxf(M, __ldcg(sh.part(p, c) + h));
+#pragma unroll
+  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
+  L = 0.0f;
+  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+  for (int c = first; c <= sh.c1; c += step) {
+    const float* pp = sh.part(p, c);
+    const float mc = __ldcg(pp + h);
+    const float f = mc == -INFINITY ? 0.0f : exp2f(mc - M);
+    const float4 x = __ldcg(reinterpret_cast<const float4*>(pp + kSpanHead + h * kD) + lane);
+    L = __fmaf_rn(f, __ldcg(pp + 16 + h), L);
+    acc.x = __fmaf_rn(f, x.x, acc.x);
+    acc.y = __fmaf_rn(f, x.y, acc.y);
+    acc.z = __fmaf_rn(f, x.z, acc.z);
+    acc.w = __fmaf_rn(f, x.w, acc.w);
+  }
+  return acc;
 }
 
 template <typename T>
@@ -628,66 +668,62 @@ __global__ void __launch_bounds__(kSpanThreads) span_join_kernel(const __grid_co
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int G = p.group;
   const int64_t total = span_index(p, index);
+  const SpanDeal deal = span_deal(total, span_ctas(total, p.n_cta));  // the attention's runs
 
   if ((int)blockIdx.x >= jp.n_mass) {
-    const int e = blockIdx.x - jp.n_mass, h = e % G, x = e / G;
-    int64_t row, row_base;
-    SpanWhere where;
-    if (jp.by_row) {
-      row = x;
-      where = span_at(p, index, x / p.n_kv_heads);
+    const int e = blockIdx.x - jp.n_mass;
+    if (jp.by_row) {  // head h of row e / G, a quarter of the partials per warp
+      const int h = e % G;
+      const int64_t row = e / G;
+      const SpanWhere where = span_at(p, index, (int)(row / p.n_kv_heads));
       if (where.units == 0) return;
-      row_base = where.base + (int64_t)(x % p.n_kv_heads) * span_cost(where.units);
-    } else {
-      const int n_cta = span_ctas(total, p.n_cta), c = x + 1;
-      if (c >= n_cta) return;
-      const int64_t cut = span_cut(total, c, n_cta);
-      where = span_find(p, index, cut);
-      const int64_t g = (cut - where.base) / span_cost(where.units);
-      row = (int64_t)where.b * p.n_kv_heads + g;
-      row_base = where.base + g * span_cost(where.units);
-      if (cut <= row_base + kSpanSetup) return;  // the row begins behind the cut
-      if (span_owner(total, row_base + kSpanSetup, n_cta) != c - 1) return;
-    }
-    const SpanShare sh = span_share(p, total, row_base, where.units);
-    if (sh.c0 == sh.c1) return;  // its CTA wrote the output
-    float M = -INFINITY;
-    for (int c = sh.c0 + lane; c <= sh.c1; c += 32) M = fmaxf(M, __ldcg(sh.part(p, c) + h));
+      const SpanShare sh =
+          span_share(p, deal, where.base + (row % p.n_kv_heads) * span_cost(where.units), where.units);
+      if (sh.c0 == sh.c1) return;  // its CTA wrote the output
+      float L;
+      const float4 acc = span_join(p, sh, h, sh.c0 + warp, kSpanWarps, lane, L);
+      *reinterpret_cast<float4*>(&s_o[warp][lane * 4]) = acc;
+      if (lane == 0) s_l[warp] = L;
+      __syncthreads();
+      float O = 0.0f;
+      L = 0.0f;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
-    float L = 0.0f;
-    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-    for (int c = sh.c0 + warp; c <= sh.c1; c += kSpanWarps) {
-      const float* pp = sh.part(p, c);
-      const float mc = __ldcg(pp + h);
-      const float f = mc == -INFINITY ? 0.0f : exp2f(mc - M);
-      const float4 x4 = __ldcg(reinterpret_cast<const float4*>(pp + kSpanHead + h * kD) + lane);
-      L = __fmaf_rn(f, __ldcg(pp + 16 + h), L);
-      acc.x = __fmaf_rn(f, x4.x, acc.x);
-      acc.y = __fmaf_rn(f, x4.y, acc.y);
-      acc.z = __fmaf_rn(f, x4.z, acc.z);
-      acc.w = __fmaf_rn(f, x4.w, acc.w);
+      for (int w = 0; w < kSpanWarps; ++w) {
+        O += s_o[w][tid];
+        L += s_l[w];
+      }
+      store_f(static_cast<T*>(p.out) + (row * G + h) * kD + tid, L == 0.0f ? 0.0f : O / L);
+      return;
     }
-    *reinterpret_cast<float4*>(&s_o[warp][lane * 4]) = acc;
-    if (lane == 0) s_l[warp] = L;
-    __syncthreads();
-    float O = 0.0f;
-    L = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kSpanWarps; ++w) {
-      O += s_o[w][tid];
-      L += s_l[w];
+    // the row that cut e + 1 goes through, a head per warp: few partials each
+    const int n_cta = span_ctas(total, p.n_cta), c = e + 1;
+    if (c >= n_cta) return;
+    const int64_t cut = deal.cut(c);
+    const SpanWhere where = span_find(p, index, cut);
+    const int64_t g = (cut - where.base) / span_cost(where.units);
+    const int64_t row = (int64_t)where.b * p.n_kv_heads + g, row_base = where.base + g * span_cost(where.units);
+    if (cut <= row_base + kSpanSetup) return;                       // its units begin behind the cut
+    if (deal.owner(row_base + kSpanSetup) != c - 1) return;         // an earlier cut's
+    const SpanShare sh = span_share(p, deal, row_base, where.units);
+    for (int h = warp; h < G; h += kSpanWarps) {
+      float L;
+      const float4 acc = span_join(p, sh, h, sh.c0, 1, lane, L);
+      const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+      T* out = static_cast<T*>(p.out) + (row * G + h) * kD + lane * 4;
+      store_f(out, acc.x * inv);
+      store_f(out + 1, acc.y * inv);
+      store_f(out + 2, acc.z * inv);
+      store_f(out + 3, acc.w * inv);
     }
-    store_f(static_cast<T*>(p.out) + (row * G + h) * kD + tid, L == 0.0f ? 0.0f : O / L);
     return;
   }
 
   // the weights of this warp's run
   const int n_run = jp.n_mass * kSpanWarps, run = blockIdx.x * kSpanWarps + warp;
   if (total == 0) return;
-  int64_t u0 = span_cut(total, run, n_run);
-  const int64_t u1 = span_cut(total, run + 1, n_run);
+  const SpanDeal runs = span_deal(total, n_run);
+  int64_t u0 = runs.cut(run);
+  const int64_t u1 = runs.cut(run + 1);
   if (u0 >= u1) return;
   const SpanWhere where = span_find(p, index, u0);
   int b = where.b;
@@ -711,7 +747,7 @@ __global__ void __launch_bounds__(kSpanThreads) span_join_kernel(const __grid_co
     const int64_t row = (int64_t)b * p.n_kv_heads + g;
     if (i1 > i0) {
       // every head's maximum and reciprocal sum: lane h holds head h's
-      const SpanShare sh = span_share(p, total, row_base, u.n);
+      const SpanShare sh = span_share(p, deal, row_base, u.n);
       float m_h = -INFINITY, r_h = 0.0f;
       if (sh.c0 == sh.c1) {
         if (lane < G) {
@@ -739,36 +775,66 @@ __global__ void __launch_bounds__(kSpanThreads) span_join_kernel(const __grid_co
         }
       }
       r_h = r_h == 0.0f ? 0.0f : 1.0f / r_h;
-      // 16 lanes a unit, four slots each
-      for (int i = i0; i < i1; i += 2) {
-        const int iu = min(i + (lane >> 4), u.n - 1);
-        const int t = u.unit(iu) * kSpanUnit + (lane & 15) * 4;
-        bool on = i + (lane >> 4) < i1 && t < v.hi && (t + 4 > v.lo || t < v.s);
-        if (on && p.pm.table != nullptr)  // slots of a lost page have no logits
-          on = (unsigned)__ldg(p.pm.table + (int64_t)b * p.pm.max_blocks + (t >> p.pm.log2bs)) <
-               (unsigned)p.pm.n_pages;
-        const float* z = p.logits + row * G * p.ld_logits + t;
-        float w[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-        for (int h = 0; h < G; ++h) {
-          const float m = __shfl_sync(0xFFFFFFFFu, m_h, h), r = __shfl_sync(0xFFFFFFFFu, r_h, h);
-          if (on) {
-            const float4 x = __ldcg(reinterpret_cast<const float4*>(z + h * p.ld_logits));
-            w[0] = __fmaf_rn(exp2f(x.x - m), r, w[0]);
-            w[1] = __fmaf_rn(exp2f(x.y - m), r, w[1]);
-            w[2] = __fmaf_rn(exp2f(x.z - m), r, w[2]);
-            w[3] = __fmaf_rn(exp2f(x.w - m), r, w[3]);
+      // 16 lanes a unit, four slots each, two units per lane at a time: all
+      // loads of a round are in flight together
+      for (int i = i0; i < i1; i += 4) {
+        int t[2];
+        bool on[2], full[2];
+        float4 y[2];
+        float w[2][4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int k = i + 2 * j + (lane >> 4);
+          t[j] = u.unit(min(k, u.n - 1)) * kSpanUnit + (lane & 15) * 4;
+          on[j] = k < i1 && t[j] < v.hi && (t[j] + 4 > v.lo || t[j] < v.s);
+          full[j] = vec && t[j] + 4 <= v.hi && (t[j] >= v.lo || t[j] + 4 <= v.s);
+          if (on[j] && full[j]) y[j] = *reinterpret_cast<const float4*>(p.mass + row * p.mass_ld + t[j]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[j][e] = 0.0f;
+        }
+        bool there[2] = {true, true};  // slots of a lost page have no logits
+        if (p.pm.table != nullptr) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            if (on[j])
+              there[j] = (unsigned)__ldg(p.pm.table + (int64_t)b * p.pm.max_blocks + (t[j] >> p.pm.log2bs)) <
+                         (unsigned)p.pm.n_pages;
+        }
+        for (int h0 = 0; h0 < G; h0 += 4) {
+          float4 x[2][4];
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+              x[j][h] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              if (on[j] && h0 + h < G)
+                x[j][h] = __ldcg(reinterpret_cast<const float4*>(p.logits + (row * G + h0 + h) * p.ld_logits + t[j]));
+            }
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            const float m = __shfl_sync(0xFFFFFFFFu, m_h, h0 + h), r = __shfl_sync(0xFFFFFFFFu, r_h, h0 + h);
+            if (h0 + h >= G) continue;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              w[j][0] = __fmaf_rn(exp2f(x[j][h].x - m), r, w[j][0]);
+              w[j][1] = __fmaf_rn(exp2f(x[j][h].y - m), r, w[j][1]);
+              w[j][2] = __fmaf_rn(exp2f(x[j][h].z - m), r, w[j][2]);
+              w[j][3] = __fmaf_rn(exp2f(x[j][h].w - m), r, w[j][3]);
+            }
           }
         }
-        if (!on) continue;
-        float* ms = p.mass + row * p.mass_ld + t;
-        if (vec && t + 4 <= v.hi && (t >= v.lo || t + 4 <= v.s)) {
-          const float4 y = *reinterpret_cast<float4*>(ms);
-          *reinterpret_cast<float4*>(ms) = make_float4(y.x + w[0], y.y + w[1], y.z + w[2], y.w + w[3]);
-        } else {
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (v.sees(t + e)) ms[e] += w[e];
+        for (int j = 0; j < 2; ++j) {
+          if (!on[j] || !there[j]) continue;
+          float* ms = p.mass + row * p.mass_ld + t[j];
+          if (full[j]) {
+            *reinterpret_cast<float4*>(ms) =
+                make_float4(y[j].x + w[j][0], y[j].y + w[j][1], y[j].z + w[j][2], y[j].w + w[j][3]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (v.sees(t[j] + e)) ms[e] += w[j][e];
+          }
         }
       }
     }

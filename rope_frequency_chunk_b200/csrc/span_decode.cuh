@@ -266,14 +266,15 @@ __global__ void __launch_bounds__(kSpanThreads, 2) span_decode_kernel(const __gr
     const int64_t total = span_index(p, index);
     const int n_cta = span_ctas(total, p.n_cta);
     if ((int)blockIdx.x >= n_cta) return;
-    const int64_t u0 = span_cut(total, blockIdx.x, n_cta);
+    const SpanDeal deal = span_deal(total, n_cta);
+    const int64_t u0 = deal.cut(blockIdx.x);
     const SpanWhere where = span_find(p, index, u0);
     use.b = where.b;
     const int64_t at = u0 - where.base;
     use.g = (int)(at / span_cost(where.units));
     const int a0 = (int)(at % span_cost(where.units));
     use.i = max(a0 - kSpanSetup, 0);
-    use.left = span_cut(total, blockIdx.x + 1, n_cta) - u0 - max(kSpanSetup - a0, 0);
+    use.left = deal.cut(blockIdx.x + 1) - u0 - max(kSpanSetup - a0, 0);
     sd_open(p, use);
   }
   SdCursor get = use;  // where the loads are

@@ -288,8 +288,8 @@ fasa_status fasa_attend_decode(const fasa_cache* c, const fasa_paged* pg, const 
   // about four CTAs per SM over the units that the rows can have
   if (mass != nullptr)
     jp.n_mass = (int)std::max<int64_t>(1, std::min<int64_t>(4LL * d.sms, ceil_div(rows * span_max_units(sp), 4)));
-  const int64_t joins = p.n_cta == 0 ? 0 : jp.by_row ? rows : p.n_cta - 1;
-  const dim3 jgrid((unsigned)(jp.n_mass + joins * p.group), 1, 1);
+  const int64_t joins = p.n_cta == 0 ? 0 : jp.by_row ? (int64_t)rows * p.group : p.n_cta - 1;
+  const dim3 jgrid((unsigned)(jp.n_mass + joins), 1, 1);
   if (jgrid.x == 0) return FASA_OK;
   return c->dtype == FASA_F32 ? launch_pdl(span_join_kernel<float>, jgrid, kSpanThreads, 0, stream, jp)
                               : launch_pdl(span_join_kernel<__nv_bfloat16>, jgrid, kSpanThreads, 0, stream, jp);
