@@ -79,31 +79,46 @@ __device__ __forceinline__ void evict_batch(const EvictParams& p, int row, uint3
         mine_d = p.pm.table ? paged_row(p.pm, b, g, td) : (int)(row * p.max_len + td);
         if (mine_d < 0) mine_s = -1;  // a page outside the pool, flagged
       }
-      // K and V: a bf16 row is half a warp's 16-byte vectors, a float32 row a
-      // whole warp's
-      const bool half = p.row16 == 16;
-      for (int r = 0; r < (half ? 1 : 2); ++r) {
-        uint4* base = static_cast<uint4*>((half ? lane >= 16 : r == 1) ? p.v : p.k);
-        const int c = half ? lane & 15 : lane;
-        uint4 x[kEvBatch];
-  #pragma unroll
-        for (int i = 0; i < kEvBatch; ++i) {
-          const int rs = __shfl_sync(0xFFFFFFFFu, mine_s, i);
-          if (rs >= 0) x[i] = __ldcs(base + (int64_t)rs * p.row16 + c);
-        }
-  #pragma unroll
-        for (int i = 0; i < kEvBatch; ++i) {
-          const int rs = __shfl_sync(0xFFFFFFFFu, mine_s, i), rd = __shfl_sync(0xFFFFFFFFu, mine_d, i);
-          if (rs >= 0) base[(int64_t)rd * p.row16 + c] = x[i];
-        }
-      }
-      uint4* sk = static_cast<uint4*>(p.sketch);
-      for (int e0 = 0; e0 < kEvBatch * p.sk16; e0 += 32) {
-        const int i = min((e0 + lane) / p.sk16, kEvBatch - 1), c = (e0 + lane) % p.sk16;
-        const int rs = __shfl_sync(0xFFFFFFFFu, mine_s, i), rd = __shfl_sync(0xFFFFFFFFu, mine_d, i);
-        if (rs >= 0 && e0 + lane < kEvBatch * p.sk16)
-          sk[(int64_t)rd * p.sk16 + c] = __ldcs(sk + (int64_t)rs * p.sk16 + c);
-      }
+      // the sketch rows' vectors, a power of two each: the first 32 of the batch
+  // are requested ahead of K and V
+  uint4* sk = static_cast<uint4*>(p.sketch);
+  const int n_sk = kEvBatch * p.sk16;
+  auto sk_at = [&](int e0, int& rs, int& rd) {
+    const int i = min((e0 + lane) / p.sk16, kEvBatch - 1);
+    rs = __shfl_sync(0xFFFFFFFFu, mine_s, i);
+    rd = __shfl_sync(0xFFFFFFFFu, mine_d, i);
+    if (e0 + lane >= n_sk) rs = -1;
+  };
+  int rs0, rd0;
+  sk_at(0, rs0, rd0);
+  const int c0 = lane % p.sk16;
+  uint4 s0 = make_uint4(0, 0, 0, 0);
+  if (rs0 >= 0) s0 = __ldcs(sk + (int64_t)rs0 * p.sk16 + c0);
+  // K and V: a bf16 row is half a warp's 16-byte vectors, a float32 row a
+  // whole warp's
+  const bool half = p.row16 == 16;
+  for (int r = 0; r < (half ? 1 : 2); ++r) {
+    uint4* base = static_cast<uint4*>((half ? lane >= 16 : r == 1) ? p.v : p.k);
+    const int c = half ? lane & 15 : lane;
+    uint4 x[kEvBatch];
+#pragma unroll
+    for (int i = 0; i < kEvBatch; ++i) {
+      const int rs = __shfl_sync(0xFFFFFFFFu, mine_s, i);
+      if (rs >= 0) x[i] = __ldcs(base + (int64_t)rs * p.row16 + c);
+    }
+#pragma unroll
+    for (int i = 0; i < kEvBatch; ++i) {
+      const int rs = __shfl_sync(0xFFFFFFFFu, mine_s, i), rd = __shfl_sync(0xFFFFFFFFu, mine_d, i);
+      if (rs >= 0) base[(int64_t)rd * p.row16 + c] = x[i];
+    }
+  }
+  if (rs0 >= 0) sk[(int64_t)rd0 * p.sk16 + c0] = s0;
+  for (int e0 = 32; e0 < n_sk; e0 += 32) {
+    int rs, rd;
+    sk_at(e0, rs, rd);
+    const int c = (e0 + lane) % p.sk16;
+    if (rs >= 0) sk[(int64_t)rd * p.sk16 + c] = __ldcs(sk + (int64_t)rs * p.sk16 + c);
+  }
 }
 
 // The lowest k set bits of x.
@@ -168,6 +183,7 @@ __global__ void __launch_bounds__(kEvThreads, 2) evict_kernel(const __grid_const
   int32_t* pos_o = p.slot_pos_out + (int64_t)row * p.max_len;
   const bool copy_m = mass_o != mass, copy_p = pos_o != pos;
   if (L <= p.budget) {  // nothing leaves (the whole cluster agrees)
+    if (p.n_moves != nullptr && rank == 0 && tid == 0) p.n_moves[row] = 0;
     for (int t = rank * kEvThreads + tid; t < L; t += C * kEvThreads) {
       if (copy_m) mass_o[t] = mass[t];
       if (copy_p) pos_o[t] = pos[t];
@@ -176,12 +192,16 @@ __global__ void __launch_bounds__(kEvThreads, 2) evict_kernel(const __grid_const
   }
   const int t0 = rank * p.chunk, n = max(0, min(L - t0, p.chunk));
   const int64_t recent = (int64_t)__ldg(p.cur_pos + b) - p.n_recent;
+  for (int i = tid; i < kEvBins; i += kEvThreads) hist[i] = 0;
+  __syncthreads();
 #pragma unroll 4
   for (int i = tid; i < n; i += kEvThreads) {
     const int x = pos[t0 + i];
     const float m = mass[t0 + i];
     const bool held = x < p.n_sink || x > recent;
-    keys[i] = held ? kEvHeld : min(score_key(m), kEvHeld - 1);
+    const uint32_t key = held ? kEvHeld : min(score_key(m), kEvHeld - 1);
+    keys[i] = key;
+    atomicAdd(&hist[key >> 21], 1u);  // the first digit
   }
 
   // the budget-th largest key, digit by digit from the top: `prefix` holds
@@ -192,13 +212,15 @@ __global__ void __launch_bounds__(kEvThreads, 2) evict_kernel(const __grid_const
 #pragma unroll
   for (int pass = 0; pass < 3; ++pass) {
     const int bins = 1 << kBits[pass];
-    for (int i = tid; i < bins; i += kEvThreads) hist[i] = 0;
-    __syncthreads();  // (first pass: the keys too)
-    const int done = kShift[pass] + kBits[pass];
-    for (int i = tid; i < n; i += kEvThreads) {
-      const uint32_t key = keys[i];
-      if (pass == 0 || (key >> done) == (prefix >> done))
-        atomicAdd(&hist[(key >> kShift[pass]) & (bins - 1)], 1u);
+    if (pass > 0) {
+      for (int i = tid; i < bins; i += kEvThreads) hist[i] = 0;
+      __syncthreads();
+      const int done = kShift[pass] + kBits[pass];
+#pragma unroll 4
+      for (int i = tid; i < n; i += kEvThreads) {
+        const uint32_t key = keys[i];
+        if ((key >> done) == (prefix >> done)) atomicAdd(&hist[(key >> kShift[pass]) & (bins - 1)], 1u);
+      }
     }
     const uint32_t* sum = hist;
     if (C > 1) {
@@ -373,7 +395,6 @@ __global__ void __launch_bounds__(kEvThreads, 2) evict_kernel(const __grid_const
 __global__ void __launch_bounds__(256) evict_move_kernel(const __grid_constant__ EvictParams p) {
   grid_dependency_wait();
   const int row = blockIdx.y;
-  if (__ldg(p.seq_len + row / p.n_kv_heads) <= p.budget) return;
   const uint32_t n_moves = (uint32_t)__ldcg(p.n_moves + row);
   const int lane = threadIdx.x & 31;
   for (uint32_t m0 = (blockIdx.x * 8 + (threadIdx.x >> 5)) * kEvBatch; m0 < n_moves; m0 += gridDim.x * 8 * kEvBatch)
