@@ -46,6 +46,7 @@ struct SpanParams {
   int32_t n_kv_heads;
   int32_t group;
   int32_t n_cta;             // CTAs the units are dealt to; 0: one CTA per row, no partials
+  int32_t tokens;            // prompts: tokens per CTA of the CUDA-core kernel, tokens * group <= MG
   PageMap pm;
   float* part;               // [2 * n_cta][kSpanHead + group * 128]: m[16], l[16], o[G][128]
   float* rstat;              // [rows][2 * group]: m, l of a row one CTA finished
@@ -314,33 +315,37 @@ __device__ __forceinline__ void span_stage_turns(const SpanParams& p, double* tu
   for (int i = threadIdx.x; i < kNFC; i += NT) turns[i] = p.turns[i];
 }
 
-// The G query rows of token (b, j), KV head g: thread's pairs (dims i, i + 64)
-// e = tid, tid + NT, ... of the G * 64, loaded (any time ahead) and rotated at
-// position pos and scaled by log2(e) / sqrt(128) into qs [G][128].
+// The G query rows of n_t tokens (b, j ..), KV head g, token by token: a
+// thread's pairs (dims i, i + 64) e = tid, tid + NT, ... of the n_t G * 64,
+// loaded (any time ahead) and rotated at positions pos .. and scaled by
+// log2(e) / sqrt(128) into qs [n_t G][128].
 template <typename T, int NT, int MG>
 struct SpanQuery {
   static constexpr int kN = (MG * kNFC + NT - 1) / NT;
   T x[kN], y[kN];
-  __device__ __forceinline__ void load(const SpanParams& p, int b, int j, int g) {
-    const T* q = static_cast<const T*>(p.q) + (((int64_t)b * p.n_q + j) * p.n_kv_heads + g) * p.group * kD;
+  __device__ __forceinline__ void load(const SpanParams& p, int b, int j, int g, int n_t = 1) {
+    const int64_t step = (int64_t)p.n_kv_heads * p.group * kD;  // from token to token
+    const T* q = static_cast<const T*>(p.q) + ((int64_t)b * p.n_q + j) * step + (int64_t)g * p.group * kD;
 #pragma unroll
     for (int n = 0; n < kN; ++n) {
-      const int e = threadIdx.x + n * NT;
-      if (e < p.group * kNFC) {
-        x[n] = q[(e / kNFC) * kD + e % kNFC];
-        y[n] = q[(e / kNFC) * kD + e % kNFC + kNFC];
+      const int e = threadIdx.x + n * NT, h = e / kNFC, t = n_t > 1 ? h / p.group : 0;
+      if (e < n_t * p.group * kNFC) {
+        const T* row = q + t * step + (h - t * p.group) * kD + e % kNFC;
+        x[n] = row[0];
+        y[n] = row[kNFC];
       }
     }
   }
-  __device__ __forceinline__ void rotate(const SpanParams& p, const double* turns, int64_t pos, float* qs) const {
+  __device__ __forceinline__ void rotate(const SpanParams& p, const double* turns, int64_t pos, float* qs,
+                                         int n_t = 1) const {
     constexpr float kScale = 1.4426950408889634f * 0.08838834764831845f;
 #pragma unroll
     for (int n = 0; n < kN; ++n) {
-      const int e = threadIdx.x + n * NT, h = e / kNFC, i = e % kNFC;
-      if (e < p.group * kNFC) {
+      const int e = threadIdx.x + n * NT, h = e / kNFC, i = e % kNFC, t = n_t > 1 ? h / p.group : 0;
+      if (e < n_t * p.group * kNFC) {
         const float a = to_float(x[n]), b = to_float(y[n]);
         float c = 1.0f, s = 0.0f;
-        if (!p.q_prerot) span_angle(turns[i], pos, &c, &s);
+        if (!p.q_prerot) span_angle(turns[i], pos + t, &c, &s);
         qs[h * kD + i] = (a * c - b * s) * kScale;
         qs[h * kD + i + kNFC] = (b * c + a * s) * kScale;
       }
@@ -349,25 +354,27 @@ struct SpanQuery {
 };
 
 // One CTA's share of a row, units [i0, i1) of the row's n: the output when
-// that is the whole row, else partial `slot`.
+// that is the whole row, else partial `slot`. A prompt's CTA takes n_t tokens
+// from j on, so that a slot's K and V serve them all; v is then the union of
+// what they see, pos the first one's position.
 template <typename T, int MG>
 __device__ __forceinline__ void span_cc_segment(const SpanParams& p, SpanCcSmem<MG>& sm, int b, int j, int g,
                                                 const Span& v, const SpanUnits& u, int64_t pos, int i0, int i1,
-                                                int slot) {
+                                                int slot, int L, int n_t) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int G = p.group;
+  const int G = p.group, R = n_t * G;  // query rows
   const int64_t row = (int64_t)b * p.n_kv_heads + g;
   __syncthreads();  // the previous segment is done with shared memory
   SpanQuery<T, kSpanThreads, MG> raw;
-  raw.load(p, b, j, g);
-  raw.rotate(p, sm.turns, pos, &sm.q[0][0]);
+  raw.load(p, b, j, g, n_t);
+  raw.rotate(p, sm.turns, pos, &sm.q[0][0], n_t);
   __syncthreads();
   float q[MG][4], o[MG][4];
 #pragma unroll
   for (int h = 0; h < MG; ++h)
 #pragma unroll
     for (int d = 0; d < 4; ++d) {
-      q[h][d] = h < G ? sm.q[h][lane * 4 + d] : 0.0f;
+      q[h][d] = h < R ? sm.q[h][lane * 4 + d] : 0.0f;
       o[h][d] = 0.0f;
     }
   // after the reduce-scatter a lane holds kMine values (slot, head) with
@@ -381,6 +388,20 @@ __device__ __forceinline__ void span_cc_segment(const SpanParams& p, SpanCcSmem<
   float l_run[kMine];  // this lane's share of the sums
 #pragma unroll
   for (int i = 0; i < kMine; ++i) l_run[i] = 0.0f;
+  // what this lane's rows see (with one token, v itself)
+  Span vi[kMine];
+  {
+    int first = 0, n = kVals;
+#pragma unroll
+    for (int o2 = 16; o2 >= 1; o2 >>= 1)
+      if (n > 1) {
+        n >>= 1;
+        if (lane & o2) first += n;
+      }
+#pragma unroll
+    for (int i = 0; i < kMine; ++i)
+      vi[i] = n_t > 1 ? span_of(L, pos + min((first % MG + i) / G, n_t - 1), p.window, p.n_sink) : v;
+  }
   const bool paged = p.pm.table != nullptr;
   const int64_t plane = paged ? 0 : row * p.max_len;
   const T* kb = static_cast<const T*>(p.k);
@@ -437,8 +458,10 @@ __device__ __forceinline__ void span_cc_segment(const SpanParams& p, SpanCcSmem<
         z[r * MG + h] = q[h][0] * k4[r].x + q[h][1] * k4[r].y + q[h][2] * k4[r].z + q[h][3] * k4[r].w;
     const int first = span_reduce_scatter<kVals>(z, lane);
     const int rz = first / MG, hz = first % MG;  // this lane's slot and first head
-    const bool seen = (ok >> rz) & 1u;
-    if (p.logits != nullptr && seen) {
+    bool seen[kMine];
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) seen[i] = ((ok >> rz) & 1u) && vi[i].sees(t0 + rz);
+    if (p.logits != nullptr && seen[0]) {
 #pragma unroll
       for (int i = 0; i < kMine; ++i)
         if (hz + i < G) p.logits[(row * G + hz + i) * p.ld_logits + t0 + rz] = z[i];
@@ -446,7 +469,7 @@ __device__ __forceinline__ void span_cc_segment(const SpanParams& p, SpanCcSmem<
     // the step's probabilities: maxima per head over the step's slots
     __syncwarp();
 #pragma unroll
-    for (int i = 0; i < kMine; ++i) sm.p[warp][rz][hz + i] = seen ? z[i] : -INFINITY;
+    for (int i = 0; i < kMine; ++i) sm.p[warp][rz][hz + i] = seen[i] ? z[i] : -INFINITY;
     __syncwarp();
 #pragma unroll
     for (int h = 0; h < MG; ++h) {
@@ -466,7 +489,7 @@ __device__ __forceinline__ void span_cc_segment(const SpanParams& p, SpanCcSmem<
 #pragma unroll
       for (int h = 0; h < MG; ++h)
         if (h == hz + i) mh = m_run[h];
-      const float pz = (seen && mh != -INFINITY) ? exp2f(z[i] - mh) : 0.0f;
+      const float pz = (seen[i] && mh != -INFINITY) ? exp2f(z[i] - mh) : 0.0f;
       l_run[i] = l_run[i] * sm.sc[warp][hz + i] + pz;
       sm.p[warp][rz][hz + i] = pz;
     }
@@ -515,49 +538,57 @@ __device__ __forceinline__ void span_cc_segment(const SpanParams& p, SpanCcSmem<
   const bool whole = i0 == 0 && i1 == u.n;
   T* out = static_cast<T*>(p.out) + (((int64_t)b * p.n_q + j) * p.n_kv_heads + g) * G * kD;
   float* pp = whole ? nullptr : p.part + (int64_t)slot * (kSpanHead + G * kD);
-  for (int e = tid; e < G * kD; e += kSpanThreads) {
-    const int h = e / kD, d = e % kD;
+  for (int e = tid; e < R * kD; e += kSpanThreads) {
+    const int h = e / kD, d = e % kD, t = n_t > 1 ? h / G : 0;
     float M = -INFINITY;
 #pragma unroll
     for (int w = 0; w < kSpanWarps; ++w) M = fmaxf(M, sm.m[w][h]);
-    float L = 0.0f, O = 0.0f;
+    float L_sum = 0.0f, O = 0.0f;
 #pragma unroll
     for (int w = 0; w < kSpanWarps; ++w) {
       const float f = sm.m[w][h] == -INFINITY ? 0.0f : exp2f(sm.m[w][h] - M);
-      L += f * sm.l[w][h];
+      L_sum += f * sm.l[w][h];
       O += f * sm.o[w][h][d];
     }
     if (whole) {
-      store_f(out + e, L == 0.0f ? 0.0f : O / L);
+      store_f(out + (int64_t)t * (p.n_kv_heads - 1) * G * kD + e, L_sum == 0.0f ? 0.0f : O / L_sum);
       if (d == 0 && p.rstat != nullptr) {
         p.rstat[row * 2 * G + h] = M;
-        p.rstat[row * 2 * G + G + h] = L;
+        p.rstat[row * 2 * G + G + h] = L_sum;
       }
     } else {
       pp[kSpanHead + e] = O;
       if (d == 0) {
         pp[h] = M;
-        pp[16 + h] = L;
+        pp[16 + h] = L_sum;
       }
     }
   }
 }
 
 // Grid: n_cta CTAs over the rows' units (decode), or with n_cta 0 one CTA per
-// (token, row): x = token, y = row (no partials).
+// (p.tokens tokens, row): x = tokens, y = row (no partials).
 template <typename T, int MG>
 __global__ void __launch_bounds__(kSpanThreads) span_cc_kernel(const __grid_constant__ SpanParams p) {
   __shared__ SpanCcSmem<MG> sm;
   span_stage_turns<kSpanThreads>(p, sm.turns);
   grid_dependency_wait();
   if (p.n_cta == 0) {
-    const int b = blockIdx.y / p.n_kv_heads, g = blockIdx.y % p.n_kv_heads, j = blockIdx.x;
+    const int b = blockIdx.y / p.n_kv_heads, g = blockIdx.y % p.n_kv_heads, j = blockIdx.x * p.tokens;
     const int L = span_len(p, b), nq = span_qlen(p, b);
     if (j >= nq) return;
+    const int n_t = min(p.tokens, nq - j);
     const int64_t pos = span_pos0(p, b, L, nq) + j;
-    const Span v = span_of(L, pos, p.window, p.n_sink);
+    // the union over the tokens: the last one's end and sinks, the first one's window
+    Span v = span_of(L, pos, p.window, p.n_sink);
+    if (n_t > 1) {
+      const Span first = span_of(L, max(pos, (int64_t)0), p.window, p.n_sink);
+      v = span_of(L, pos + n_t - 1, p.window, p.n_sink);
+      v.lo = min(first.lo, v.hi);
+      v.s = min(v.s, v.lo);
+    }
     const SpanUnits u = span_units(v, kSpanUnit);
-    span_cc_segment<T, MG>(p, sm, b, j, g, v, u, pos, 0, u.n, 0);
+    span_cc_segment<T, MG>(p, sm, b, j, g, v, u, pos, 0, u.n, 0, L, n_t);
     return;
   }
   span_zero_rows<T, kSpanThreads>(p);
@@ -584,7 +615,7 @@ __global__ void __launch_bounds__(kSpanThreads) span_cc_kernel(const __grid_cons
     }
     const int a1 = (int)min((int64_t)span_cost(u.n), a0 + (u1 - u0));
     const int i0 = max(a0 - kSpanSetup, 0), i1 = a1 - kSpanSetup;
-    if (i1 > i0) span_cc_segment<T, MG>(p, sm, b, 0, g, v, u, pos, i0, i1, 2 * blockIdx.x + (first ? 0 : 1));
+    if (i1 > i0) span_cc_segment<T, MG>(p, sm, b, 0, g, v, u, pos, i0, i1, 2 * blockIdx.x + (first ? 0 : 1), L, 1);
     first = false;
     u0 += a1 - a0;
     a0 = 0;

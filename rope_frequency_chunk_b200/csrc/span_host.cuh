@@ -63,6 +63,7 @@ void span_fill(SpanParams& p, const fasa_cache* c, const fasa_paged* pg, const f
   p.n_sink = sp->n_sink;
   p.q_prerot = sp->q_prerotated;
   p.n_q = n_q;
+  p.tokens = 1;
   p.batch = c->batch;
   p.n_kv_heads = c->n_kv_heads;
   p.group = c->n_q_heads / c->n_kv_heads;
@@ -75,6 +76,7 @@ struct SpanCc {
   const void* fn;
   void (*kern)(const SpanParams);
 };
+// G: query rows of a CTA.
 template <typename T>
 SpanCc span_cc_pick(int G) {
   if (G == 1) return {(const void*)span_cc_kernel<T, 1>, span_cc_kernel<T, 1>};
@@ -85,7 +87,8 @@ SpanCc span_cc_pick(int G) {
 }
 
 fasa_status span_cc_launch(SpanParams& p, int dtype, dim3 grid, cudaStream_t st) {
-  const SpanCc k = dtype == FASA_F32 ? span_cc_pick<float>(p.group) : span_cc_pick<__nv_bfloat16>(p.group);
+  const int rows = p.group * p.tokens;
+  const SpanCc k = dtype == FASA_F32 ? span_cc_pick<float>(rows) : span_cc_pick<__nv_bfloat16>(rows);
   return launch_pdl(k.kern, grid, kSpanThreads, 0, st, p);
 }
 
@@ -316,7 +319,10 @@ fasa_status fasa_attend_prompt(const fasa_cache* c, const fasa_paged* pg, const 
   if (span_tensor_cores(c, pg)) return launch_prompt(c, pg, sp, q, n_q, out, workspace, d, stream);
   SpanParams p{};
   span_fill(p, c, pg, sp, q, out, n_q);
-  const dim3 grid((unsigned)n_q, (unsigned)(c->batch * c->n_kv_heads), 1);
+  // tokens share a CTA up to 8 query rows, while that leaves every SM two CTAs
+  const int64_t rows = (int64_t)c->batch * c->n_kv_heads;
+  while (2 * p.tokens * p.group <= 8 && ceil_div(n_q, 2 * p.tokens) * rows >= 2LL * d.sms) p.tokens *= 2;
+  const dim3 grid((unsigned)ceil_div(n_q, p.tokens), (unsigned)rows, 1);
   return span_cc_launch(p, c->dtype, grid, stream);
 }
 

@@ -302,6 +302,14 @@ def test_prompt_f32(lens, nq, window):
     prompt_case(lens, nq, 3, 1, F32, window=window, n_sink=3)
 
 
+@pytest.mark.parametrize("hq,hkv", [(2, 2), (4, 2), (9, 3), (8, 2), (10, 2)])
+def test_prompt_f32_tokens_sharing_a_block(hq, hkv):
+    """Enough tokens that up to eight share a CTA; windows end between them."""
+    prompt_case([900, 300], [900, 77], hq, hkv, F32, window=37, n_sink=5, block=32)
+    prompt_case([1300], [1201], hq, hkv, F32)
+    prompt_case([700], [700], hq, hkv, F32, q_pos=[-9], window=64, n_sink=3, prerot=True)
+
+
 def test_prompt_one_query_is_the_decode():
     f = S.Filled([900, 65], 8, 2, BF, 16)
     q = (S.randn(f.g, 2, 8, 128) * 1.5).to(BF)
