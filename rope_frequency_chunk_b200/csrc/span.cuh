@@ -10,8 +10,9 @@
 // computed in one pass with a running maximum and sum in float32, base 2.
 //
 // Here: the span and the work partition shared by the kernels, the CUDA-core
-// kernel (float32 caches, and caches in host memory) and the join of rows that
-// several CTAs shared, which also adds the slots' attention weights.
+// kernel (float32 decode and short prompts, and caches in host memory) and the
+// join of rows that several CTAs shared, which also adds the slots' attention
+// weights.
 #pragma once
 
 #include "fasa_device.cuh"

@@ -104,6 +104,30 @@ bool span_tensor_cores(const fasa_cache* c, const fasa_paged* pg) {
   return c->dtype == FASA_BF16 && span_rows(c, pg) < INT32_MAX && !host_resident(c->k) && !host_resident(c->v);
 }
 
+// float32 prompts: the tiled kernel, or the CUDA-core one. A tile takes the
+// same time however many of its 64 rows hold queries, the CUDA-core kernel's
+// time goes with the query rows per SM: the tiles win from 24 rows per SM and
+// wave of tiles on. Over 2000 slots (tiles, CUDA cores): 128 tokens 32/8 heads
+// 333, 345 us; 64 tokens 323, 239 us; 16 x 8 tokens 8/8 heads 313, 194 us, 16
+// x 32 tokens 317, 376 us; 16 x 16 tokens 32/8 heads 319, 714 us.
+constexpr int64_t kTiRowsPerSm = 24;
+bool span_tiled(const SpanParams& p, const DevInfo& d) {
+  const int64_t rows = (int64_t)p.batch * p.n_kv_heads;
+  const int64_t waves = ceil_div(ceil_div(p.n_q, kTiRows / p.group) * rows, d.sms);
+  return rows * p.group * p.n_q >= kTiRowsPerSm * waves * d.sms;
+}
+fasa_status launch_tile(const SpanParams& p, cudaStream_t st) {
+  int set = 0;
+  fasa_status s = cached_int((const void*)span_tile_kernel, 0, &set, [&](int* v) {
+    *v = 1;
+    return cuda_status(
+        cudaFuncSetAttribute(span_tile_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(TiSmem)));
+  });
+  if (s != FASA_OK) return s;
+  const dim3 grid((unsigned)ceil_div(p.n_q, kTiRows / p.group), (unsigned)(p.batch * p.n_kv_heads), 1);
+  return launch_pdl(span_tile_kernel, grid, kTiThreads, sizeof(TiSmem), st, p);
+}
+
 // A bf16 tensor read in boxes stored for the 128-byte swizzle (64 elements
 // wide); rows out of range read as zeros. strides: bytes, of dimensions 1 ..
 fasa_status span_encode(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
@@ -319,6 +343,7 @@ fasa_status fasa_attend_prompt(const fasa_cache* c, const fasa_paged* pg, const 
   if (span_tensor_cores(c, pg)) return launch_prompt(c, pg, sp, q, n_q, out, workspace, d, stream);
   SpanParams p{};
   span_fill(p, c, pg, sp, q, out, n_q);
+  if (c->dtype == FASA_F32 && span_tiled(p, d)) return launch_tile(p, stream);
   // tokens share a CTA up to 8 query rows, while that leaves every SM two CTAs
   const int64_t rows = (int64_t)c->batch * c->n_kv_heads;
   while (2 * p.tokens * p.group <= 8 && ceil_div(n_q, 2 * p.tokens) * rows >= 2LL * d.sms) p.tokens *= 2;

@@ -310,6 +310,15 @@ def test_prompt_f32_tokens_sharing_a_block(hq, hkv):
     prompt_case([700], [700], hq, hkv, F32, q_pos=[-9], window=64, n_sink=3, prerot=True)
 
 
+@pytest.mark.parametrize("hq,hkv,nq", [(2, 2, 900), (1, 1, 1200), (6, 2, 590), (16, 1, 200), (16, 1, 250), (14, 2, 300),
+                                       (32, 2, 130)])
+def test_prompt_f32_few_and_many_rows(hq, hkv, nq):
+    """Query rows below and above one tile's worth per SM; lengths inside a page, ragged batches, a row of none."""
+    prompt_case([nq + 33, 0, 40], [nq, 5, 40], hq, hkv, F32, window=0, block=16)
+    prompt_case([nq + 33], [nq], hq, hkv, F32, window=70, n_sink=130, block=64)
+    prompt_case([nq], [nq], hq, hkv, F32, q_pos=[150], window=100, n_sink=3)
+
+
 def test_prompt_one_query_is_the_decode():
     f = S.Filled([900, 65], 8, 2, BF, 16)
     q = (S.randn(f.g, 2, 8, 128) * 1.5).to(BF)
