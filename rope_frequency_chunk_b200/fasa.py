@@ -142,6 +142,28 @@ def _stream(stream) -> int | None:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _new(stream, device, make, returned=False):
+    """make(), a tensor for a call that launches on `stream`. The allocator
+    hands a freed block out again in the order of the stream that was current
+    when it was allocated, so the launch stream is made current: the block is
+    neither still in use by another stream's work nor reused under the launch.
+    A tensor that goes back to the caller is also kept from reuse until what
+    the caller's own stream does with it is done."""
+    if stream is None:
+        return make()
+    current = torch.cuda.current_stream(device)
+    handle = _stream(stream)
+    if handle == current.cuda_stream:
+        return make()
+    if not hasattr(stream, "cuda_stream"):  # a raw handle; 0 and 1 name the default stream
+        stream = torch.cuda.ExternalStream(handle, device) if handle > 1 else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        t = make()
+    if returned:
+        t.record_stream(current)
+    return t
+
+
 def _ptr(t: torch.Tensor | None):
     return None if t is None else t.data_ptr()
 
@@ -288,13 +310,13 @@ def fasa_decode_paged(cache: PagedKVCache, seq_len, q, max_seq_len: int, max_bud
     _q(cache, q)
     vl = _varlen(seq_len, budget, max_seq_len, max_budget, q_prerotated)
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(stream, q.device, lambda: torch.empty_like(q), True)
     _dev(out, "out", cache.dtype)
     if idx_out is not None:
         _dev(idx_out, "idx_out", torch.int32)
     if workspace is None:
         need = int(lib().fasa_decode_paged_workspace_bytes(cache.ref(), cache.pref(), ctypes.byref(vl)))
-        workspace = torch.zeros(max(need, 1), dtype=torch.uint8, device=q.device)
+        workspace = _new(stream, q.device, lambda: torch.zeros(max(need, 1), dtype=torch.uint8, device=q.device))
     _dev(workspace, "workspace", torch.uint8)
     _check(lib().fasa_decode_paged(cache.ref(), cache.pref(), ctypes.byref(vl), q.data_ptr(), out.data_ptr(),
                                    _ptr(idx_out), workspace.data_ptr(), workspace.numel(), _stream(stream)),
@@ -324,7 +346,8 @@ def _q(cache, q):
 def fasa_score(cache: KVCache, length: int, q, q_pos: int, scores=None, stream=None):
     _q(cache, q)
     if scores is None:
-        scores = torch.empty(cache.batch, cache.n_kv_heads, length, dtype=torch.float32, device=q.device)
+        scores = _new(stream, q.device, lambda: torch.empty(cache.batch, cache.n_kv_heads, length, dtype=torch.float32,
+                                                            device=q.device), True)
     _dev(scores, "scores", torch.float32)
     _check(lib().fasa_score(cache.ref(), length, q.data_ptr(), q_pos, scores.data_ptr(), _stream(stream)),
            "fasa_score")
@@ -337,7 +360,8 @@ def fasa_select_topk(scores, k: int, idx=None, stream=None):
     rows = scores.numel() // max(length, 1)
     k_eff = min(k, length)
     if idx is None:
-        idx = torch.empty(*scores.shape[:-1], k_eff, dtype=torch.int32, device=scores.device)
+        idx = _new(stream, scores.device, lambda: torch.empty(*scores.shape[:-1], k_eff, dtype=torch.int32,
+                                                              device=scores.device), True)
     _dev(idx, "idx", torch.int32)
     _check(lib().fasa_select_topk(scores.data_ptr(), rows, length, k, idx.data_ptr(), _stream(stream)),
            "fasa_select_topk")
@@ -348,7 +372,7 @@ def fasa_sparse_attend(cache: KVCache, length: int, q, q_pos: int, idx, out=None
     _q(cache, q)
     _dev(idx, "idx", torch.int32)
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(stream, q.device, lambda: torch.empty_like(q), True)
     _dev(out, "out", cache.dtype)
     _check(lib().fasa_sparse_attend(cache.ref(), length, q.data_ptr(), q_pos, idx.data_ptr(), idx.shape[-1],
                                     out.data_ptr(), _stream(stream)), "fasa_sparse_attend")
@@ -372,13 +396,13 @@ def fasa_decode(cache: KVCache, length: int, q, q_pos: int, k: int, out=None, id
     given workspace must have been zeroed once (fasa_decode_workspace)."""
     _q(cache, q)
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(stream, q.device, lambda: torch.empty_like(q), True)
     _dev(out, "out", cache.dtype)
     if idx_out is not None:
         _dev(idx_out, "idx_out", torch.int32)
     need = fasa_decode_workspace_bytes(cache, length, k)
     if workspace is None:
-        workspace = torch.zeros(max(need, 1), dtype=torch.uint8, device=q.device)
+        workspace = _new(stream, q.device, lambda: torch.zeros(max(need, 1), dtype=torch.uint8, device=q.device))
     _dev(workspace, "workspace", torch.uint8)
     _check(lib().fasa_decode(cache.ref(), length, q.data_ptr(), q_pos, k, out.data_ptr(), _ptr(idx_out),
                              workspace.data_ptr(), workspace.numel(), _stream(stream)), "fasa_decode")
@@ -419,12 +443,13 @@ def fasa_decode_varlen(cache: KVCache, seq_len, q, max_seq_len: int, max_budget:
     _q(cache, q)
     vl = _varlen(seq_len, budget, max_seq_len, max_budget, q_prerotated)
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(stream, q.device, lambda: torch.empty_like(q), True)
     _dev(out, "out", cache.dtype)
     if idx_out is not None:
         _dev(idx_out, "idx_out", torch.int32)
     if workspace is None:
-        workspace = fasa_decode_varlen_workspace(cache, max_seq_len, max_budget, q.device)
+        workspace = _new(stream, q.device,
+                         lambda: fasa_decode_varlen_workspace(cache, max_seq_len, max_budget, q.device))
     _dev(workspace, "workspace", torch.uint8)
     _check(lib().fasa_decode_varlen(cache.ref(), ctypes.byref(vl), q.data_ptr(), out.data_ptr(), _ptr(idx_out),
                                     workspace.data_ptr(), workspace.numel(), _stream(stream)),
@@ -448,12 +473,12 @@ def fasa_decode_multi(cache: KVCache, length: int, q, q_pos0: int, k: int, out=N
         raise ValueError("q must be [B, n_q, Hq, 128]")
     n_q = q.shape[1]
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(stream, q.device, lambda: torch.empty_like(q), True)
     _dev(out, "out", cache.dtype)
     if idx_out is not None:
         _dev(idx_out, "idx_out", torch.int32)
     if workspace is None:
-        workspace = fasa_decode_multi_workspace(cache, length, n_q, k, q.device)
+        workspace = _new(stream, q.device, lambda: fasa_decode_multi_workspace(cache, length, n_q, k, q.device))
     _dev(workspace, "workspace", torch.uint8)
     _check(lib().fasa_decode_multi(cache.ref(), length, q.data_ptr(), q_pos0, n_q, k, out.data_ptr(),
                                    _ptr(idx_out), workspace.data_ptr(), workspace.numel(), _stream(stream)),
@@ -539,11 +564,12 @@ def fasa_attend_decode(cache, seq_len, q, max_seq_len: int, window: int = 0, n_s
     _q(cache, q)
     sp = _span(cache, seq_len, max_seq_len, window, n_sink, q_pos, None, q_prerotated)
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(stream, q.device, lambda: torch.empty_like(q), True)
     _same(_dev(out, "out", cache.dtype), q)
     m = _per_slot(cache, mass, "mass", torch.float32)
     if workspace is None:
-        workspace = fasa_attend_decode_workspace(cache, max_seq_len, mass is not None, q.device)
+        workspace = _new(stream, q.device,
+                         lambda: fasa_attend_decode_workspace(cache, max_seq_len, mass is not None, q.device))
     _dev(workspace, "workspace", torch.uint8)
     _launch("fasa_attend_decode", q, stream, cache.ref(), _pages(cache), ctypes.byref(sp), q.data_ptr(),
             out.data_ptr(), m, workspace.data_ptr(), workspace.numel())
@@ -574,10 +600,10 @@ def fasa_attend_prompt(cache, seq_len, q, max_seq_len: int, window: int = 0, n_s
     n_q = q.shape[1]
     sp = _span(cache, seq_len, max_seq_len, window, n_sink, q_pos, q_len, q_prerotated)
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(stream, q.device, lambda: torch.empty_like(q), True)
     _same(_dev(out, "out", cache.dtype), q)
     if workspace is None:
-        workspace = fasa_attend_prompt_workspace(cache, n_q, max_seq_len, q.device)
+        workspace = _new(stream, q.device, lambda: fasa_attend_prompt_workspace(cache, n_q, max_seq_len, q.device))
     _dev(workspace, "workspace", torch.uint8)
     _launch("fasa_attend_prompt", q, stream, cache.ref(), _pages(cache), ctypes.byref(sp), q.data_ptr(), n_q,
             out.data_ptr(), workspace.data_ptr(), workspace.numel())
@@ -615,10 +641,11 @@ def fasa_evict(cache, seq_len, cur_pos, mass, slot_pos, max_seq_len: int, budget
     mo = mp if mass_out is None else _per_slot(cache, mass_out, "mass_out", torch.float32)
     so = sp if slot_pos_out is None else _per_slot(cache, slot_pos_out, "slot_pos_out", torch.int32)
     if len_out is None:
-        len_out = torch.empty_like(seq_len)
+        len_out = _new(stream, seq_len.device, lambda: torch.empty_like(seq_len), True)
     lo = _per_seq(cache, len_out, "len_out")
     if workspace is None:
-        workspace = fasa_evict_workspace(cache, max_seq_len, budget, seq_len.device)
+        workspace = _new(stream, seq_len.device,
+                         lambda: fasa_evict_workspace(cache, max_seq_len, budget, seq_len.device))
     _dev(workspace, "workspace", torch.uint8)
     _launch("fasa_evict", seq_len, stream, cache.ref(), _pages(cache), ctypes.byref(d), mp, sp, mo, so, lo,
             workspace.data_ptr(), workspace.numel())
@@ -678,10 +705,10 @@ def fasa_dense_decode(cache: KVCache, length: int, q, q_pos: int, out=None, work
     given workspace must have been zeroed once (fasa_dense_workspace)."""
     _q(cache, q)
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(stream, q.device, lambda: torch.empty_like(q), True)
     _dev(out, "out", cache.dtype)
     if workspace is None:
-        workspace = fasa_dense_workspace(cache, length, q.device)
+        workspace = _new(stream, q.device, lambda: fasa_dense_workspace(cache, length, q.device))
     _dev(workspace, "workspace", torch.uint8)
     _check(lib().fasa_dense_decode(cache.ref(), length, q.data_ptr(), q_pos, out.data_ptr(), workspace.data_ptr(),
                                    workspace.numel(), _stream(stream)), "fasa_dense_decode")
@@ -715,8 +742,9 @@ def fasa_calibrate_scores(cache: KVCache, length: int, q_win, q_pos0: int, plane
     """Score planes [B, Hkv, n_win, 65, len] float32 of the calibration queries."""
     n_win = _q_win(cache, q_win)
     if planes is None:
-        planes = torch.empty(cache.batch, cache.n_kv_heads, n_win, CAL_PLANES, length, dtype=torch.float32,
-                             device=q_win.device)
+        planes = _new(stream, q_win.device,
+                      lambda: torch.empty(cache.batch, cache.n_kv_heads, n_win, CAL_PLANES, length,
+                                          dtype=torch.float32, device=q_win.device), True)
     _dev(planes, "planes", torch.float32)
     _check(lib().fasa_calibrate_scores(cache.ref(), length, q_win.data_ptr(), q_pos0, n_win, planes.data_ptr(),
                                        _stream(stream)), "fasa_calibrate_scores")
@@ -731,11 +759,13 @@ def fasa_calibrate_counts(planes, n_kv_heads: int, budget: int, counts=None, wor
         raise ValueError("planes must be [..., n_win, 65, len]")
     rows = planes.numel() // (n_win * CAL_PLANES * length)
     if counts is None:
-        counts = torch.empty(n_kv_heads, 64, dtype=torch.int32, device=planes.device)
+        counts = _new(stream, planes.device,
+                      lambda: torch.empty(n_kv_heads, 64, dtype=torch.int32, device=planes.device), True)
     _dev(counts, "counts", torch.int32)
     need = rows * n_win * CAL_PLANES * min(budget, length) * 4
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=planes.device)
+        workspace = _new(stream, planes.device,
+                         lambda: torch.empty(max(need, 1), dtype=torch.uint8, device=planes.device))
     _dev(workspace, "workspace", torch.uint8)
     _check(lib().fasa_calibrate_counts(planes.data_ptr(), rows, n_kv_heads, n_win, length, budget,
                                        counts.data_ptr(), workspace.data_ptr(), workspace.numel(),
@@ -747,7 +777,8 @@ def fasa_calibrate_dominant(counts, n_dom: int, dom_idx=None, stream=None):
     """I_dom [Hkv, n_dom] int32 from counts [Hkv, 64]."""
     _dev(counts, "counts", torch.int32)
     if dom_idx is None:
-        dom_idx = torch.empty(counts.shape[0], n_dom, dtype=torch.int32, device=counts.device)
+        dom_idx = _new(stream, counts.device, lambda: torch.empty(counts.shape[0], n_dom, dtype=torch.int32,
+                                                                  device=counts.device), True)
     _dev(dom_idx, "dom_idx", torch.int32)
     _check(lib().fasa_calibrate_dominant(counts.data_ptr(), counts.shape[0], n_dom, dom_idx.data_ptr(),
                                          _stream(stream)), "fasa_calibrate_dominant")
@@ -760,14 +791,14 @@ def fasa_calibrate(cache: KVCache, length: int, q_win, q_pos0: int, budget: int,
     n_win = _q_win(cache, q_win)
     dev = q_win.device
     if counts is None:
-        counts = torch.empty(cache.n_kv_heads, 64, dtype=torch.int32, device=dev)
+        counts = _new(stream, dev, lambda: torch.empty(cache.n_kv_heads, 64, dtype=torch.int32, device=dev), True)
     if dom_idx is None:
-        dom_idx = torch.empty(cache.n_kv_heads, n_dom, dtype=torch.int32, device=dev)
+        dom_idx = _new(stream, dev, lambda: torch.empty(cache.n_kv_heads, n_dom, dtype=torch.int32, device=dev), True)
     _dev(counts, "counts", torch.int32)
     _dev(dom_idx, "dom_idx", torch.int32)
     need = fasa_calibrate_workspace_bytes(cache, length, n_win, budget)
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+        workspace = _new(stream, dev, lambda: torch.empty(max(need, 1), dtype=torch.uint8, device=dev))
     _dev(workspace, "workspace", torch.uint8)
     _check(lib().fasa_calibrate(cache.ref(), length, q_win.data_ptr(), q_pos0, n_win, budget, n_dom,
                                 counts.data_ptr(), dom_idx.data_ptr(), workspace.data_ptr(), workspace.numel(),
