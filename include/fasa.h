@@ -636,7 +636,9 @@ fasa_status fasa_attend_prompt(const fasa_cache* cache, const fasa_paged* pages,
  *  budget >= 1 and n_sink + n_recent <= budget; max_seq_len <= FASA_MAX_LEN.
  *  pages   : NULL, or a paged cache whose pages belong to one sequence each.
  *            A move from or to a page outside the pool is flagged
- *            FASA_ERR_BAD_INDEX and left out.
+ *            FASA_ERR_BAD_INDEX and left out: the slot it would have filled
+ *            keeps its own row, weight and position (in mass_out and
+ *            slot_pos_out too), and the kept token behind the budget is lost.
  *  workspace : at least fasa_evict_workspace_bytes bytes, 256-byte aligned,
  *            plain scratch.
  *  Errors: bad sizes or pointers -> FASA_ERR_INVALID_ARG; max_seq_len beyond

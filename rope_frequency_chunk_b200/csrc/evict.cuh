@@ -70,16 +70,25 @@ __device__ __forceinline__ void evict_batch(const EvictParams& p, int row, uint3
   const int32_t* dst = src + p.max_moves;
   const float* mass = p.mass + (int64_t)row * p.max_len;
   const int32_t* pos = p.slot_pos + (int64_t)row * p.max_len;
-      int mine_s = -1, mine_d = -1;  // lane i < kEvBatch: the rows of move m0 + i
-      if (lane < kEvBatch && m0 + lane < n_moves) {
-        const int ts = __ldcg(src + m0 + lane), td = __ldcg(dst + m0 + lane);
-        p.mass_out[(int64_t)row * p.max_len + td] = mass[ts];
-        p.slot_pos_out[(int64_t)row * p.max_len + td] = pos[ts];
-        mine_s = p.pm.table ? paged_row(p.pm, b, g, ts) : (int)(row * p.max_len + ts);
-        mine_d = p.pm.table ? paged_row(p.pm, b, g, td) : (int)(row * p.max_len + td);
-        if (mine_d < 0) mine_s = -1;  // a page outside the pool, flagged
-      }
-      // the sketch rows' vectors, a power of two each: the first 32 of the batch
+  // lane i < kEvBatch: the rows of move m0 + i. A move from or to a page outside
+  // the pool (flagged) is left out whole: its target slot keeps its own row,
+  // and with it its own weight and position.
+  int mine_s = -1, mine_d = -1;
+  if (lane < kEvBatch && m0 + lane < n_moves) {
+    const int ts = __ldcg(src + m0 + lane), td = __ldcg(dst + m0 + lane);
+    float m = mass[ts];
+    int x = pos[ts];
+    mine_s = p.pm.table ? paged_row(p.pm, b, g, ts) : (int)(row * p.max_len + ts);
+    mine_d = p.pm.table ? paged_row(p.pm, b, g, td) : (int)(row * p.max_len + td);
+    if (mine_s < 0 || mine_d < 0) {
+      mine_s = -1;
+      m = mass[td];
+      x = pos[td];
+    }
+    p.mass_out[(int64_t)row * p.max_len + td] = m;
+    p.slot_pos_out[(int64_t)row * p.max_len + td] = x;
+  }
+  // the sketch rows' vectors, a power of two each: the first 32 of the batch
   // are requested ahead of K and V
   uint4* sk = static_cast<uint4*>(p.sketch);
   const int n_sk = kEvBatch * p.sk16;

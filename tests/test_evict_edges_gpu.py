@@ -1,0 +1,66 @@
+"""Evictions at their edges: pages outside the pool, the largest share of one
+CTA, few and many moves."""
+
+import numpy as np
+import pytest
+import torch
+
+from rope_frequency_chunk_b200 import fasa as F
+from tests import span_util as S
+
+pytestmark = pytest.mark.gpu
+BF = torch.bfloat16
+
+
+@pytest.fixture(autouse=True)
+def _clean_status():
+    F.fasa_device_status(clear=True)
+    yield
+    assert F.fasa_device_status(clear=True) == 0
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device=S.DEV)
+
+
+@pytest.mark.parametrize("inplace", [True, False])
+@pytest.mark.parametrize("L,budget,block,lost", [(300, 100, 16, "source"), (300, 100, 16, "target"),
+                                                 (300, 100, 16, "both"), (9000, 4400, 64, "source"),
+                                                 (9000, 4400, 64, "target")])
+def test_moves_of_lost_pages_are_left_out_whole(L, budget, block, lost, inplace):
+    """K, V, sketch, weights and positions against the plain form without
+    exactly the moves that touch a lost page (few moves in one launch, many in
+    two)."""
+    hkv = 3
+    f = S.Filled([L, L - 7], 2 * hkv, hkv, BF, block)
+    c = f.cache
+    m = torch.rand(2, hkv, c.max_len, generator=f.g, device=S.DEV)
+    pos = torch.stack([torch.stack([torch.randperm(c.max_len, generator=f.g, device=S.DEV) for _ in range(hkv)])
+                       for _ in range(2)]).int()
+    gone = {"source": [budget // block + 2], "target": [1], "both": [1, 4, budget // block + 2]}[lost]
+    for i, blk in enumerate(gone):
+        c.block_table[0, blk] = [-1, c.n_pages, 2 ** 31 - 1][i]
+    want = [x.clone() for x in (c.k, c.v, c.sketch)]
+    mo = m if inplace else torch.full_like(m, 5.0)
+    po = pos if inplace else torch.full_like(pos, 5)
+    want_m, want_p = mo.clone(), po.clone()
+    for b, n in enumerate(f.lens):
+        for g in range(hkv):
+            src = np.array(S.evict_plain(m[b, g].tolist(), pos[b, g].tolist(), n, n - 1, budget, 4, 20))
+            dst = np.arange(len(src))
+            if b == 0:
+                bad = (src != dst) & (np.isin(src // block, gone) | np.isin(dst // block, gone))
+                assert bad.any() and (bad.sum() < (src != dst).sum())
+                src = np.where(bad, dst, src)  # a slot whose move is left out keeps its own
+            s, d = torch.from_numpy(src).to(S.DEV), torch.from_numpy(dst).to(S.DEV)
+            want_m[b, g, :budget], want_p[b, g, :budget] = m[b, g, s], pos[b, g, s]
+            mv = s != d
+            ps, pd = c.block_table[b, s[mv] // block].long(), c.block_table[b, d[mv] // block].long()
+            for w, x in zip(want, (c.k, c.v, c.sketch)):
+                w[pd, g, d[mv] % block] = x[ps, g, s[mv] % block]
+    n = F.fasa_evict(c, f.seq_len, f.seq_len - 1, m, pos, L, budget, n_sink=4, n_recent=20,
+                     mass_out=None if inplace else mo, slot_pos_out=None if inplace else po)
+    assert F.fasa_device_status(clear=True) == 7 and n.tolist() == [budget, budget]
+    assert torch.equal(mo, want_m) and torch.equal(po, want_p)
+    for w, x in zip(want, (c.k, c.v, c.sketch)):
+        assert torch.equal(w.nan_to_num(9.0), x.nan_to_num(9.0))
