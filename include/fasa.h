@@ -583,7 +583,9 @@ fasa_status fasa_attend_decode(const fasa_cache* cache, const fasa_paged* pages,
                                const void* q, void* out, float* mass, void* workspace, size_t workspace_bytes,
                                cudaStream_t stream);
 
-/* Workspace bytes fasa_attend_prompt needs (0 for invalid arguments). */
+/* Workspace bytes fasa_attend_prompt needs for 1 .. n_q queries (0 for invalid
+ * arguments). The size for a max_seq_len without a window serves every shorter
+ * one, with or without a window. */
 size_t fasa_attend_prompt_workspace_bytes(const fasa_cache* cache, const fasa_span* span, int32_t n_q);
 
 /*

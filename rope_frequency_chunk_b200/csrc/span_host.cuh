@@ -324,7 +324,15 @@ fasa_status fasa_attend_decode(const fasa_cache* c, const fasa_paged* pg, const 
 
 size_t fasa_attend_prompt_workspace_bytes(const fasa_cache* c, const fasa_span* sp, int32_t n_q) {
   if (check_cache(c) != FASA_OK || check_span(c, sp) != FASA_OK || n_q < 1) return 0;
-  return prompt_layout(c, sp, n_q, kAssumedMaxSms).bytes;
+  // the largest over 1 .. n_q queries: fewer of them make fewer items, which
+  // are cut into more parts. Sizes go by tiles per row, and parts only exist
+  // while the items fill half the SMs or fewer.
+  const int per = 2 * pr_tokens(c->n_q_heads / c->n_kv_heads);
+  const int64_t rows = (int64_t)c->batch * c->n_kv_heads;
+  size_t bytes = prompt_layout(c, sp, n_q, kAssumedMaxSms).bytes;
+  for (int64_t t = 1; t * rows * 2 <= kAssumedMaxSms && t * per < n_q; ++t)
+    bytes = std::max(bytes, prompt_layout(c, sp, (int32_t)(t * per), kAssumedMaxSms).bytes);
+  return bytes;
 }
 
 fasa_status fasa_attend_prompt(const fasa_cache* c, const fasa_paged* pg, const fasa_span* sp, const void* q,
@@ -336,7 +344,8 @@ fasa_status fasa_attend_prompt(const fasa_cache* c, const fasa_paged* pg, const 
   if ((s = check_span(c, sp)) != FASA_OK) return s;
   if (n_q < 1 || !aligned(q, 16) || !aligned(out, 16)) return FASA_ERR_INVALID_ARG;
   if (n_q > FASA_MAX_LEN) return FASA_ERR_UNSUPPORTED;
-  const size_t need = fasa_attend_prompt_workspace_bytes(c, sp, n_q);
+  // what this call uses, which may be less than the size for up to n_q queries
+  const size_t need = prompt_layout(c, sp, n_q, kAssumedMaxSms).bytes;
   if (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < need) return FASA_ERR_WORKSPACE;
   DevInfo d;
   if ((s = device_info(&d)) != FASA_OK) return s;

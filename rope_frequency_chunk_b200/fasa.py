@@ -582,9 +582,11 @@ def _same(out, q):
 
 
 def fasa_attend_prompt_workspace(cache, n_q: int, max_seq_len: int, device=None):
-    """A workspace for fasa_attend_prompt up to this length, any window."""
+    """A workspace for fasa_attend_prompt of up to n_q queries per sequence
+    and up to this length, any window."""
     dev = device if device is not None else cache.sketch.device
-    return _scratch(int(lib().fasa_attend_prompt_workspace_bytes(cache.ref(), ctypes.byref(_bounds(max_seq_len)), int(n_q))),
+    return _scratch(int(lib().fasa_attend_prompt_workspace_bytes(cache.ref(), ctypes.byref(_bounds(max_seq_len)),
+                                                             int(n_q))),
                     "fasa_attend_prompt_workspace_bytes", dev)
 
 
