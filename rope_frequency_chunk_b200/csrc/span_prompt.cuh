@@ -420,23 +420,32 @@ __device__ __forceinline__ float pr_top(const uint32_t* s, int n) {
 constexpr float kPrScale = 1.4426950408889634f * 0.08838834764831845f;  // log2(e) / sqrt(128)
 
 // The two warps of a row quadrant meet at a named barrier. A warp whose wait
-// for the tensor core gave up still comes, having raised `failed`, and both
-// leave together: neither is left at the barrier.
+// for the tensor core gave up still comes, having raised the block's `failed`,
+// and both leave together. The barrier itself carries the vote: read behind
+// it, the word could be raised (by any warp of the block) between the two
+// warps' reads, and the one that stayed would wait at the barrier for good.
 struct PrPair {
   int id;                 // barrier 1 .. 8
   volatile int* failed;   // one word for the block
   volatile float* mine;   // this thread's slot, the other thread's
   volatile float* other;
 };
-__device__ __forceinline__ void pr_meet(const PrPair& pr) {
-  asm volatile("barrier.cta.sync %0, 64;" ::"r"(pr.id) : "memory");
+// False, to both warps, once either of them has seen `failed` raised.
+__device__ __forceinline__ bool pr_meet(const PrPair& pr) {
+  uint32_t gone;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.s32 q, %2, 0;\n barrier.cta.red.or.pred p, %1, 64, q;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(gone)
+      : "r"(pr.id), "r"(*pr.failed)
+      : "memory");
+  return gone == 0;
 }
 // The larger of the two threads' values. The slots are free again once both
 // warps have handed over P, before the next S.
 __device__ __forceinline__ float pr_join(float x, const PrPair& pr, bool& ok) {
   *pr.mine = x;
-  pr_meet(pr);
-  ok = *pr.failed == 0;
+  ok = pr_meet(pr);
   return pr_max(x, *pr.other);
 }
 
@@ -702,10 +711,9 @@ __global__ void __launch_bounds__(kPrThreads, 1) span_prompt_kernel(const __grid
       tc_fence_after();
       // the row's sum, once both threads are past their last exchange
       *pr.mine = row.l;
-      pr_meet(pr);
+      ok = pr_meet(pr);
       const float l = row.l + *pr.other;
-      ok = *failed == 0;
-      pr_meet(pr);
+      if (!pr_meet(pr)) ok = false;  // the slots are free again
       if (!ok) break;
       if (p.splits == 1) {
         // rows of the lane's group of four: lane k stores the k-th 16 bytes
