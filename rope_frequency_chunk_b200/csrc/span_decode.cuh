@@ -410,7 +410,9 @@ __global__ void __launch_bounds__(kSpanThreads, 2) span_decode_kernel(const __gr
         }
       }
     };
-    __syncthreads();  // every warp has its query fragments: the buffer is free
+    // every warp has its query fragments: the buffer is free. If a warp's wait
+    // gave up, all leave behind this row: none is left at a barrier.
+    ok = __syncthreads_and(ok);
     if (warp >= 2) put(warp - 2);
     __syncthreads();
     if (warp < 2) take(warp);
