@@ -490,7 +490,8 @@ __device__ __forceinline__ void span_cc_segment(const SpanParams& p, SpanCcSmem<
 #pragma unroll
       for (int h = 0; h < MG; ++h)
         if (h == hz + i) mh = m_run[h];
-      const float pz = (seen[i] && mh != -INFINITY) ? exp2f(z[i] - mh) : 0.0f;
+      // no maximum yet: -inf logits have no weight, a NaN keeps its own
+      const float pz = seen[i] ? exp2f(z[i] - (mh == -INFINITY ? 0.0f : mh)) : 0.0f;
       l_run[i] = l_run[i] * sm.sc[warp][hz + i] + pz;
       sm.p[warp][rz][hz + i] = pz;
     }

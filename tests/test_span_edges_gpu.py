@@ -1,6 +1,8 @@
 """The span attention at its edges: workspaces made for other calls, lost
 pages, values that are not finite."""
 
+import math
+
 import pytest
 import torch
 
@@ -8,7 +10,7 @@ from rope_frequency_chunk_b200 import fasa as F
 from tests import span_util as S
 
 pytestmark = pytest.mark.gpu
-BF = torch.bfloat16
+BF, F32 = torch.bfloat16, torch.float32
 
 
 @pytest.fixture(autouse=True)
@@ -28,3 +30,52 @@ def test_one_prompt_workspace_for_every_chunk():
         out = F.fasa_attend_prompt(f.cache, f.seq_len, q, 3000, window=window, n_sink=3, workspace=ws)
         ref, _, size, z = S.attend64(f, 0, q[0], list(range(3000 - n_q, 3000)), window, 3, False)
         S.check_out(out[0], ref, size, z, 3000, p_rel=2.0 ** -8)
+
+
+def not_finite(f, run, n_q, hq):
+    """NaN in one query head (of one token), then in the only key that a row
+    sees: NaN in exactly the outputs that depend on it."""
+    B = len(f.lens)
+    q = (S.randn(f.g, B, n_q, hq, 128) * 1.5).to(f.cache.dtype)
+    good = run(f.seq_len, q)
+    assert torch.isfinite(good).all()
+    q[0, n_q // 2, 1, 5] = math.nan
+    out = run(f.seq_len, q)
+    bad = torch.zeros(B, n_q, hq, dtype=torch.bool, device=S.DEV)
+    bad[0, n_q // 2, 1] = True
+    assert torch.isnan(out[bad]).all() and torch.equal(out[~bad], good[~bad])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("lens", [[40, 7], [1, 3], [900, 300]])
+def test_nan_queries_stay_nan_in_the_decode(lens, dtype):
+    f = S.Filled(lens, 8, 2, dtype, 16)
+    not_finite(f, lambda n, q: F.fasa_attend_decode(f.cache, n, q[:, 0].contiguous(), max(lens))[:, None], 1, 8)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n_q", [1, 9, 600])
+def test_nan_queries_stay_nan_in_prompts(n_q, dtype):
+    f = S.Filled([700, 650], 8, 2, dtype, 16)
+    not_finite(f, lambda n, q: F.fasa_attend_prompt(f.cache, n, q, 700), n_q, 8)
+
+
+def test_nan_queries_stay_nan_on_host_resident_caches():
+    c = F.KVCache(1, 8, 2, 4, 400, BF, S.BASE, [[0, 1, 2, 3]] * 2, kv_on_host=True)
+    f = S.Filled([390], 8, 2, BF, cap=400)
+    c.k.copy_(f.cache.k)
+    c.v.copy_(f.cache.v)
+    torch.cuda.synchronize()
+    not_finite(f, lambda n, q: F.fasa_attend_decode(c, n, q[:, 0].contiguous(), 400)[:, None], 1, 8)
+    not_finite(f, lambda n, q: F.fasa_attend_prompt(c, n, q, 400), 9, 8)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_a_nan_key_that_is_all_a_row_sees(dtype):
+    f = S.Filled([1, 300], 4, 2, dtype, 16)
+    f.put(f.cache.k, 0, torch.tensor([0], device=S.DEV), torch.full((2, 1, 128), math.nan, device=S.DEV).to(dtype))
+    q = (S.randn(f.g, 2, 4, 128) * 1.5).to(dtype)
+    m = torch.zeros(2, 2, f.cache.max_len, device=S.DEV)
+    out = F.fasa_attend_decode(f.cache, f.seq_len, q, 300, mass=m)
+    assert torch.isnan(out[0]).all() and torch.isfinite(out[1]).all()
+    assert torch.isnan(m[0, :, 0]).all() and torch.isfinite(m[1]).all()
