@@ -634,7 +634,8 @@ fasa_status fasa_attend_prompt(const fasa_cache* cache, const fasa_paged* pages,
  *  mass_out, slot_pos_out : the same shape; each either the input itself (in
  *            place) or memory apart from it. Entries 0 .. n-1 of a row are
  *            written, the others left.
- *  len_out : device [B] int32, n of every sequence; not seq_len itself.
+ *  len_out : device [B] int32, n of every sequence; apart from seq_len and
+ *            cur_pos.
  *  budget >= 1 and n_sink + n_recent <= budget; max_seq_len <= FASA_MAX_LEN.
  *  pages   : NULL, or a paged cache whose pages belong to one sequence each.
  *            A move from or to a page outside the pool is flagged

@@ -390,6 +390,12 @@ fasa_status check_evict(const fasa_cache* c, const fasa_evict_desc* e) {
   return FASA_OK;
 }
 
+// Whether two arrays share memory without being the same one.
+bool entangled(const void* a, const void* b, size_t bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x != y && (x > y ? x - y : y - x) < bytes;
+}
+
 // Up to this many moves at most the selection's own warps do them; more take a
 // launch of their own (measured: 64 rows of 32 moves 9.6 us in one launch; 8
 // rows of 7700 moves 55.8 us in one).
@@ -420,7 +426,14 @@ fasa_status fasa_evict(const fasa_cache* c, const fasa_paged* pg, const fasa_evi
   if ((s = check_evict(c, e)) != FASA_OK) return s;
   if (span_rows(c, pg) > INT32_MAX) return FASA_ERR_UNSUPPORTED;  // rows are addressed with 32-bit indices
   if (!aligned(mass, 4) || !aligned(slot_pos, 4) || !aligned(mass_out, 4) || !aligned(slot_pos_out, 4) ||
-      !aligned(len_out, 4) || len_out == e->seq_len)
+      !aligned(len_out, 4))
+    return FASA_ERR_INVALID_ARG;
+  // every row of a sequence reads its length and position while one of them
+  // writes the new length; shifted outputs would overwrite other rows' inputs
+  const size_t per_seq = (size_t)c->batch * 4, per_slot = (size_t)c->batch * c->n_kv_heads * c->max_len * 4;
+  if (len_out == e->seq_len || len_out == e->cur_pos || entangled(len_out, e->seq_len, per_seq) ||
+      entangled(len_out, e->cur_pos, per_seq) || entangled(mass_out, mass, per_slot) ||
+      entangled(slot_pos_out, slot_pos, per_slot))
     return FASA_ERR_INVALID_ARG;
   const size_t need = fasa_evict_workspace_bytes(c, e);
   if (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < need) return FASA_ERR_WORKSPACE;
