@@ -500,6 +500,14 @@ def _launch(name, t, stream, *args) -> None:
         _check(status, name)
 
 
+def _home(cache, **tensors):
+    """Every given tensor lies on the cache's device: the kernels read both."""
+    dev = cache.sketch.get_device()
+    for name, t in tensors.items():
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{name} must be on the cache's device ({cache.sketch.device}), got {t.device}")
+
+
 def _pages(cache):
     """The block table's description of a PagedKVCache, None for a KVCache."""
     return cache.pref() if isinstance(cache, PagedKVCache) else None
@@ -571,6 +579,7 @@ def fasa_attend_decode(cache, seq_len, q, max_seq_len: int, window: int = 0, n_s
         workspace = _new(stream, q.device,
                          lambda: fasa_attend_decode_workspace(cache, max_seq_len, mass is not None, q.device))
     _dev(workspace, "workspace", torch.uint8)
+    _home(cache, q=q, seq_len=seq_len, q_pos=q_pos, mass=mass, out=out, workspace=workspace)
     _launch("fasa_attend_decode", q, stream, cache.ref(), _pages(cache), ctypes.byref(sp), q.data_ptr(),
             out.data_ptr(), m, workspace.data_ptr(), workspace.numel())
     return out
@@ -607,6 +616,7 @@ def fasa_attend_prompt(cache, seq_len, q, max_seq_len: int, window: int = 0, n_s
     if workspace is None:
         workspace = _new(stream, q.device, lambda: fasa_attend_prompt_workspace(cache, n_q, max_seq_len, q.device))
     _dev(workspace, "workspace", torch.uint8)
+    _home(cache, q=q, seq_len=seq_len, q_pos=q_pos, q_len=q_len, out=out, workspace=workspace)
     _launch("fasa_attend_prompt", q, stream, cache.ref(), _pages(cache), ctypes.byref(sp), q.data_ptr(), n_q,
             out.data_ptr(), workspace.data_ptr(), workspace.numel())
     return out
@@ -649,6 +659,8 @@ def fasa_evict(cache, seq_len, cur_pos, mass, slot_pos, max_seq_len: int, budget
         workspace = _new(stream, seq_len.device,
                          lambda: fasa_evict_workspace(cache, max_seq_len, budget, seq_len.device))
     _dev(workspace, "workspace", torch.uint8)
+    _home(cache, seq_len=seq_len, cur_pos=cur_pos, mass=mass, slot_pos=slot_pos, mass_out=mass_out,
+          slot_pos_out=slot_pos_out, len_out=len_out, workspace=workspace)
     _launch("fasa_evict", seq_len, stream, cache.ref(), _pages(cache), ctypes.byref(d), mp, sp, mo, so, lo,
             workspace.data_ptr(), workspace.numel())
     return len_out
@@ -667,6 +679,7 @@ def fasa_append_kv_at(cache, k_new, v_new, slot0, pos0, slot_pos=None, mass=None
         raise TypeError("slot0 and pos0 must be CUDA tensors")
     s0, p0 = _per_seq(cache, slot0, "slot0"), _per_seq(cache, pos0, "pos0")
     sp, m = _per_slot(cache, slot_pos, "slot_pos", torch.int32), _per_slot(cache, mass, "mass", torch.float32)
+    _home(cache, k_new=k_new, v_new=v_new, slot0=slot0, pos0=pos0, slot_pos=slot_pos, mass=mass)
     _launch("fasa_append_kv_at", k_new, stream, cache.ref(), _pages(cache), k_new.data_ptr(), v_new.data_ptr(), n_new,
             s0, p0, sp, m)
 
