@@ -136,9 +136,17 @@ def _check(status: int, call: str):
         raise FasaError(status, call + detail)
 
 
+# The current device, and its current stream's handle without a Stream object
+# around it: about a microsecond less per call than the public functions, which
+# serve where torch has no such shortcuts.
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_handle = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
+           or (lambda device: torch.cuda.current_stream(device).cuda_stream))
+
+
 def _stream(stream) -> int | None:
-    if stream is None:  # the current stream's handle, without a Stream object around it
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    if stream is None:
+        return _handle(_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -492,7 +500,7 @@ def _launch(name, t, stream, *args) -> None:
     """Calls name(*args, stream) with tensor t's device current (the library
     launches on the current device)."""
     dev = t.get_device()
-    if dev != torch._C._cuda_getDevice():
+    if dev != _device():
         with torch.cuda.device(dev):
             return _launch(name, t, stream, *args)
     status = getattr(lib(), name)(*args, _stream(stream))
