@@ -19,6 +19,11 @@
 
 namespace fasa {
 
+// Hint: bring a tensor map (a kernel parameter) into the descriptor cache.
+__device__ __forceinline__ void prefetch_tensor_map(const void* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
 constexpr int kSpanUnit = 64;      // slots per unit of work
 constexpr int kSpanSetup = 2;      // cost of taking up a row (queries, join), in units
 constexpr int kSpanThreads = 128;  // 4 warps
