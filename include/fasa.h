@@ -557,9 +557,10 @@ size_t fasa_attend_decode_workspace_bytes(const fasa_cache* cache, const fasa_sp
  * Attention of one new token per sequence over its span, contiguous (pages
  * NULL) or paged. The visible slots of all rows are dealt to the GPU's CTAs
  * in equal shares, so sequences of very different lengths finish together; a
- * row that several CTAs share is joined by a second launch. Rows short enough
- * for one CTA each (max_seq_len, or the window and the sinks, within 256
- * slots) take one launch.
+ * row that several CTAs share is joined by a second launch. Where no row can
+ * touch more than four units of 64 slots (max_seq_len <= 256, or
+ * ceil(window / 64) + ceil(n_sink / 64) <= 3: the window may begin inside a
+ * unit), each row is one CTA's, and without weights one launch does it.
  *
  *  q_pos   : span->q_pos, or NULL: the query of sequence b sits at position
  *            seq_len[b], as in fasa_decode_varlen. span->q_len is not read.
@@ -568,7 +569,11 @@ size_t fasa_attend_decode_workspace_bytes(const fasa_cache* cache, const fasa_sp
  *  mass    : nullable; [B][Hkv][max_len] float32. Each visible slot's
  *            attention weight, summed over the group's query heads, is added
  *            to it: mass[b][g][t] += sum_h softmax_t(...). Other slots are left
- *            as they are. This is what fasa_evict goes by.
+ *            as they are. This is what fasa_evict goes by. Prompts add no
+ *            weights: straight after fasa_attend_prompt they are what they
+ *            were, and if all are equal an eviction keeps the lowest slots.
+ *            The weights of a prompt's last tokens come from this call, a
+ *            token at a time with its q_pos.
  *  workspace : at least fasa_attend_decode_workspace_bytes bytes, 256-byte
  *            aligned; plain scratch (no initial value, nothing kept between
  *            calls). Calls that overlap on the GPU must not share one.

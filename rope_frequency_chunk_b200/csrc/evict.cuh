@@ -15,9 +15,10 @@
 // of its share of the slots in shared memory; three histogram passes (11 + 11
 // + 10 bits, summed over the cluster through distributed shared memory) give
 // the exact budget-th largest key; ballots turn the slots into bit words, one
-// word per thread from then on; scans number the holes and the moves, and warps copy
-// the moved rows, eight at a time with all their loads in flight. Bound by memory: 8 bytes a slot and the moved rows; small rows by
-// the chain of barriers.
+// word per thread from then on; scans number the holes and the moves, and
+// warps copy the moved rows, eight at a time with all their loads in flight.
+// Bound by memory: 8 bytes a slot and the moved rows; small rows by the chain
+// of barriers.
 #pragma once
 
 #include <cooperative_groups.h>

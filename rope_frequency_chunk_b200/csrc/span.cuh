@@ -116,8 +116,10 @@ __device__ __forceinline__ int64_t span_pos0(const SpanParams& p, int b, int L, 
 }
 
 // cos and sin of pos * theta for turns = theta / (2 pi): whole turns drop out
-// in float64, so the float32 argument keeps its precision at any position
-// (angle error below 3e-7 for positions up to 2^31).
+// in float64, so the float32 argument keeps its precision. The angle is off by
+// at most 1e-7 + pos * 4e-16 rad: half a step of the float32 argument (2^-26
+// turns), and theta, 1 / (2 pi), their product and the turns rounded once each
+// in float64 (3.5 * 2^-53 of the angle); 9.3e-7 at position 2^31.
 __device__ __forceinline__ void span_angle(double turns, int64_t pos, float* c, float* s) {
   const double t = (double)pos * turns;
   sincospif(2.0f * (float)(t - rint(t)), s, c);

@@ -65,7 +65,7 @@ struct PromptParams {
   float* part;               // [B * Hkv * tiles_max * splits][256][2 + 128]: m, l planes, then o
 };
 
-// Bytes of a split's partial: m[256], l[256], o[256][128].
+// Floats of a split's partial: m[256], l[256], o[256][128].
 constexpr int64_t kPrPart = kPrRows * (2 + kD);
 
 template <int TERMS>

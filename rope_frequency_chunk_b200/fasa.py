@@ -576,7 +576,8 @@ def fasa_attend_decode(cache, seq_len, q, max_seq_len: int, window: int = 0, n_s
     the last `window` positions and the first n_sink slots. cache: a KVCache
     or a PagedKVCache; seq_len (and q_pos, default seq_len): int32 [B] on the
     device. mass, when given, is float32 [B, Hkv, max_len]: every visible
-    slot's attention weight, summed over the group's heads, is added to it."""
+    slot's attention weight, summed over the group's heads, is added to it
+    (prompts add none)."""
     _q(cache, q)
     sp = _span(cache, seq_len, max_seq_len, window, n_sink, q_pos, None, q_prerotated)
     if out is None:
@@ -638,7 +639,8 @@ def _evict_desc(cache, seq_len, cur_pos, max_seq_len, budget, n_sink, n_recent):
 
 
 def fasa_evict_workspace(cache, max_seq_len: int, budget: int, device=None):
-    """A workspace for fasa_evict at these bounds."""
+    """A workspace for fasa_evict at this budget and up to this length (other
+    budgets, smaller ones too, can need more)."""
     dev = device if device is not None else cache.sketch.device
     d = fasa_evict_desc(16, 16, int(max_seq_len), int(budget), 0, 0)
     return _scratch(int(lib().fasa_evict_workspace_bytes(cache.ref(), ctypes.byref(d))),
