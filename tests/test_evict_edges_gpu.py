@@ -64,3 +64,58 @@ def test_moves_of_lost_pages_are_left_out_whole(L, budget, block, lost, inplace)
     assert torch.equal(mo, want_m) and torch.equal(po, want_p)
     for w, x in zip(want, (c.k, c.v, c.sketch)):
         assert torch.equal(w.nan_to_num(9.0), x.nan_to_num(9.0))
+
+
+def kept_order(mass, pos, L, cur, budget, n_sink, n_recent):
+    """evict_plain, sorted by numpy (long rows)."""
+    t = np.arange(L)
+    held = (pos[:L] < n_sink) | (pos[:L] > cur - n_recent)
+    order = np.lexsort((t, np.where(held, 0.0, -mass[:L].astype(np.float64)), ~held))
+    n = min(L, budget)
+    kept = np.zeros(L, bool)
+    kept[order[:n]] = True
+    src = np.arange(n)
+    src[~kept[:n]] = t[n:][kept[n:]]
+    return src
+
+
+def test_the_two_plain_forms_agree():
+    g = torch.Generator(S.DEV).manual_seed(0)
+    for L, budget in ((50, 20), (50, 50), (50, 49), (7, 1)):
+        m = torch.randint(0, 4, (L,), generator=g, device=S.DEV).float().cpu().numpy()
+        p = torch.randperm(L, generator=g, device=S.DEV).cpu().numpy()
+        rest = (L, L - 1, budget, min(2, budget - 1), min(5, budget // 2))
+        assert kept_order(m, p, *rest).tolist() == S.evict_plain(m.tolist(), p.tolist(), *rest)
+
+
+@pytest.mark.parametrize("values", ["heavy", "few", "equal"])
+@pytest.mark.parametrize("B,hkv,L", [(25, 3, 32768), (19, 2, 65536), (19, 2, 32801)])
+def test_the_largest_share_of_one_block(B, hkv, L, values):
+    """Rows enough that a row has as few CTAs as can hold it: one of 32768
+    slots, two of 32768 each, two just above one's share."""
+    lens = [L - 37 * b for b in range(B)]
+    f = S.Filled(lens, hkv, hkv, BF, cap=L, n_dom=1)
+    c = f.cache
+    if values == "heavy":  # attention weights: most tiny, a few large
+        m = torch.rand(B, hkv, L, generator=f.g, device=S.DEV).pow_(30)
+    elif values == "few":
+        m = torch.randint(0, 3, (B, hkv, L), generator=f.g, device=S.DEV).float()
+    else:
+        m = torch.full((B, hkv, L), 0.25, device=S.DEV)
+    pos = torch.argsort(torch.rand(B, hkv, L, generator=f.g, device=S.DEV), -1).int()
+    for budget in (L - 1, L // 2, 1):  # each from the rows that the last one kept
+        n_sink, n_recent = min(4, budget - 1), min(200, budget // 2)
+        old = [x.clone() for x in (c.k, c.v, c.sketch)]
+        m0, p0 = m.clone(), pos.clone()
+        n = F.fasa_evict(c, f.seq_len, i32([L - 1] * B), m, pos, L, budget, n_sink=n_sink, n_recent=n_recent)
+        mc, pc = m0.cpu().numpy(), p0.cpu().numpy()
+        for b in range(B):
+            for g in range(hkv):
+                src = kept_order(mc[b, g], pc[b, g], f.lens[b], L - 1, budget, n_sink, n_recent)
+                s = torch.from_numpy(src).to(S.DEV)
+                k = len(src)
+                assert torch.equal(m[b, g, :k], m0[b, g, s]) and torch.equal(pos[b, g, :k], p0[b, g, s])
+                for x, was in zip((c.k, c.v, c.sketch), old):
+                    assert torch.equal(x[b, g, :k], was[b, g, s])
+        assert n.tolist() == [min(x, budget) for x in f.lens]
+        f.lens, f.seq_len = n.tolist(), n

@@ -79,3 +79,64 @@ def test_a_nan_key_that_is_all_a_row_sees(dtype):
     out = F.fasa_attend_decode(f.cache, f.seq_len, q, 300, mass=m)
     assert torch.isnan(out[0]).all() and torch.isfinite(out[1]).all()
     assert torch.isnan(m[0, :, 0]).all() and torch.isfinite(m[1]).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("block,gone", [(16, [2]), (16, [8, 9, 10, 11, 12, 13, 14, 15]), (64, [1, 6]), (256, [1]),
+                                        (128, [0]), (16, [43])])
+@pytest.mark.parametrize("n_q,window", [(1, 0), (40, 0), (640, 0), (300, 260)])
+def test_lost_pages_are_left_out_of_prompts(block, gone, n_q, window, dtype):
+    """Against float64 over the slots that are left: pages of a part of a block
+    of slots, whole blocks, the first and the last page."""
+    L = 700
+    f = S.Filled([L, 90], 8, 2, dtype, block)
+    q = (S.randn(f.g, 2, n_q, 8, 128) * 1.5).to(dtype)
+    n = [n_q, min(n_q, 90)]
+    keep = torch.ones(L, dtype=torch.bool, device=S.DEV)
+    for pg in gone:
+        keep[pg * block:(pg + 1) * block] = False
+    k, v = f.rows(f.cache.k, 0, L).double(), f.rows(f.cache.v, 0, L).double()
+    for i, pg in enumerate(gone):
+        f.cache.block_table[0, pg] = [-1, f.cache.n_pages, -2 ** 31, 2 ** 31 - 1][i % 4]
+    out = F.fasa_attend_prompt(f.cache, f.seq_len, q, L, window=window, n_sink=3, q_len=torch.tensor(
+        n, dtype=torch.int32, device=S.DEV))
+    p = torch.arange(L - n_q, L, device=S.DEV)
+    see = S.visible(L, p, window, 3)
+    # a page that no query sees is not looked up, and so not flagged
+    assert F.fasa_device_status(clear=True) == (7 if (see & ~keep).any() else 0)
+    see &= keep
+    x = S.rotate64(q[0].double(), p)
+    ref = torch.zeros(n_q, 8, 128, dtype=torch.float64, device=S.DEV)
+    size, z_max = torch.zeros_like(ref), 0.0
+    for h in range(8):
+        z = (x[:, h] @ k[h // 4].T / math.sqrt(128)).masked_fill(~see, -math.inf)
+        w = torch.softmax(z, 1).nan_to_num(0.0)
+        ref[:, h], size[:, h] = w @ v[h // 4], w @ v[h // 4].abs()
+        z_max = max(z_max, float((x[:, h].abs() @ k[h // 4].abs().T).max()) / math.sqrt(128))
+    S.check_out(out[0], ref, size, z_max, L, p_rel=2.0 ** -8)
+    r1, _, s1, z1 = S.attend64(f, 1, q[1, :n[1]], list(range(90 - n[1], 90)), window, 3, False)
+    S.check_out(out[1, :n[1]], r1, s1, z1, 90, p_rel=2.0 ** -8)
+
+
+def test_weights_that_are_not_16_byte_aligned():
+    f = S.Filled([1000, 260], 8, 2, BF, 16)
+    q = (S.randn(f.g, 2, 8, 128) * 1.5).to(BF)
+    a = torch.zeros(2, 2, f.cache.max_len, device=S.DEV)
+    b = torch.zeros(a.numel() + 1, device=S.DEV)[1:].view_as(a)
+    assert b.data_ptr() % 16 == 4
+    for m in (a, b):
+        F.fasa_attend_decode(f.cache, f.seq_len, q, 1000, window=500, n_sink=3, mass=m)
+    assert torch.equal(a, b) and (a.sum(-1) - 4).abs().max() < 1e-3
+
+
+@pytest.mark.parametrize("n_q", [3, 700])
+def test_f32_prompts_on_host_resident_caches(n_q):
+    c = F.KVCache(1, 8, 2, 4, 800, F32, S.BASE, [[0, 1, 2, 3]] * 2, kv_on_host=True)
+    f = S.Filled([790], 8, 2, F32, cap=800)
+    c.k.copy_(f.cache.k)
+    c.v.copy_(f.cache.v)
+    torch.cuda.synchronize()
+    q = S.randn(f.g, 1, n_q, 8, 128) * 1.5
+    out = F.fasa_attend_prompt(c, f.seq_len, q, 800, window=300, n_sink=3)
+    ref, _, size, z = S.attend64(f, 0, q[0], list(range(790 - n_q, 790)), 300, 3, False)
+    S.check_out(out[0], ref, size, z, 790)
