@@ -396,10 +396,15 @@ bool entangled(const void* a, const void* b, size_t bytes) {
   return x != y && (x > y ? x - y : y - x) < bytes;
 }
 
-// Up to this many moves at most the selection's own warps do them; more take a
-// launch of their own (measured: 64 rows of 32 moves 9.6 us in one launch; 8
-// rows of 7700 moves 55.8 us in one).
-constexpr int64_t kEvMovesHere = 8192;
+// The selection's own warps move the rows while each has one batch at most and
+// all rows' CTAs run at once; else the moves are a launch of their own. One
+// launch against two, us on the GPU over cold caches: 64 rows of 8 moves 8.3,
+// 8.9; of 32 11.7, 10.7; of 128 13.2, 12.2; 8 rows of 256 18.5, 11.3, of 1024
+// 42.6, 24.2; 512 rows of 20 24.8, 18.6. The second launch costs the host 2.2
+// us: eager calls of up to 128 moves a row take 11.1 to 12.2 us against 13.5.
+bool evict_moves_here(int rows, int max_moves, int sms) {
+  return max_moves <= kEvWarps * kEvBatch && rows <= 2 * sms;
+}
 
 // A kept slot behind the budget fills a hole before it: at most the smaller
 // of the two sides.
@@ -462,7 +467,7 @@ fasa_status fasa_evict(const fasa_cache* c, const fasa_paged* pg, const fasa_evi
   p.row16 = kD * elem_bytes(c->dtype) / 16;
   p.sk16 = c->sketch_stride * elem_bytes(c->dtype) / 16;
   p.pm = page_map(c, pg);
-  if ((int64_t)rows * p.max_moves > kEvMovesHere) p.n_moves = static_cast<int32_t*>(workspace);
+  if (!evict_moves_here(rows, p.max_moves, d.sms)) p.n_moves = static_cast<int32_t*>(workspace);
   // CTAs per row: enough for a CTA's share of the keys to fit, more while the
   // rows leave SMs idle and a CTA's share stays above 2048 slots
   int C = pow2ceil(ceil_div(e->max_seq_len, kEvMaxChunk));

@@ -119,3 +119,25 @@ def test_the_largest_share_of_one_block(B, hkv, L, values):
                     assert torch.equal(x[b, g, :k], was[b, g, s])
         assert n.tolist() == [min(x, budget) for x in f.lens]
         f.lens, f.seq_len = n.tolist(), n
+
+
+@pytest.mark.parametrize("B,hkv,L,budget", [(42, 8, 70, 64), (38, 4, 400, 272), (38, 4, 401, 272)])
+def test_rows_and_moves_at_the_limits_of_one_launch(B, hkv, L, budget):
+    """Few moves of more rows than run at once; 128 and 129 moves a row."""
+    lens = [L] * B
+    f = S.Filled(lens, hkv, hkv, BF, 16)
+    c = f.cache
+    m = torch.rand(B, hkv, c.max_len, generator=f.g, device=S.DEV)
+    m[:, :, budget:] += 2.0  # every slot behind the budget stays: as many moves as there can be
+    pos = torch.argsort(torch.rand(B, hkv, c.max_len, generator=f.g, device=S.DEV), -1).int()
+    m0, p0 = m.clone(), pos.clone()
+    old = [[f.rows(x, b, L).clone() for x in (c.k, c.v, c.sketch)] for b in range(B)]
+    F.fasa_evict(c, f.seq_len, i32([L - 1] * B), m, pos, L, budget)
+    for b in range(B):
+        for g in range(hkv):
+            src = kept_order(m0[b, g].cpu().numpy(), p0[b, g].cpu().numpy(), L, L - 1, budget, 0, 0)
+            assert (src >= budget).sum() == L - budget
+            s = torch.from_numpy(src).to(S.DEV)
+            assert torch.equal(m[b, g, :budget], m0[b, g, s]) and torch.equal(pos[b, g, :budget], p0[b, g, s])
+            for x, was in zip((c.k, c.v, c.sketch), old[b]):
+                assert torch.equal(f.rows(x, b, budget)[g], was[g, s])
