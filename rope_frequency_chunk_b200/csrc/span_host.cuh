@@ -26,7 +26,14 @@ int64_t span_max_units(const fasa_span* sp) {
 }
 
 // Rows of up to this many units are one CTA's work each: no partials, and no
-// second launch to join them.
+// second launch to join them. One CTA a row against units dealt to all CTAs, us
+// on the GPU over cold caches (32/8 heads): 256 bf16 slots of 1, 8, 64 sequences
+// 7.6, 8.2, 21.8 against 10.7, 12.2, 27.3; 256 float32 slots 16.2, 16.9, 40.8
+// against 19.9, 21.6, 54.8. For few sequences the two meet at 384 (float32) to
+// 512 (bf16) slots and part fast (1024: 18.7 against 12.0, 53 against 21). 64
+// equally long ones would gain from one CTA at any length (2048 slots 88
+// against 99), but the lengths are the device's and a batch of unequal ones
+// would wait for its longest.
 constexpr int kSpanWholeUnits = 4;
 constexpr int kSpanMaxPerSm = 4;  // resident CTAs per SM, an upper bound
 
@@ -106,11 +113,12 @@ bool span_tensor_cores(const fasa_cache* c, const fasa_paged* pg) {
 
 // float32 prompts: the tiled kernel, or the CUDA-core one. A tile takes the
 // same time however many of its 64 rows hold queries, the CUDA-core kernel's
-// time goes with the query rows per SM: the tiles win from 24 rows per SM and
-// wave of tiles on. Over 2000 slots (tiles, CUDA cores): 128 tokens 32/8 heads
-// 333, 345 us; 64 tokens 323, 239 us; 16 x 8 tokens 8/8 heads 313, 194 us, 16
-// x 32 tokens 317, 376 us; 16 x 16 tokens 32/8 heads 319, 714 us.
-constexpr int64_t kTiRowsPerSm = 24;
+// time goes with the query rows per SM: the tiles win from 18 rows per SM and
+// wave of tiles on. Over 2000 slots (tiles, CUDA cores): 300 tokens 8/8 heads
+// (16 rows per SM) 312, 296 us; 100 tokens 28/4 heads (19) 312, 331 us; 96 and
+// 128 tokens 32/8 heads (21, 28) 312, 340 us; 64 tokens (14) 312, 173 us; 16 x
+// 16 and 16 x 32 tokens 8/8 heads (14, 28) 314, 196 and 317, 360 us.
+constexpr int64_t kTiRowsPerSm = 18;
 bool span_tiled(const SpanParams& p, const DevInfo& d) {
   const int64_t rows = (int64_t)p.batch * p.n_kv_heads;
   const int64_t waves = ceil_div(ceil_div(p.n_q, kTiRows / p.group) * rows, d.sms);
@@ -166,7 +174,11 @@ fasa_status span_map_q(CUtensorMap* m, const void* q, int64_t n_tokens, int hq, 
 
 // Work items of a prompt call and the parts their blocks are cut into: one
 // part while the items fill half the SMs or more; else enough parts to fill
-// them, each with four blocks or more.
+// them, each with four blocks or more, 32 at most (a lane of the join each).
+// Uncut and cut, 32/8 heads: 5 queries on 8192 slots 150, 23 us, 64 on 65536
+// 1216, 99, 256 on 4096 86, 40. Parts of two, four and eight blocks or more: 1
+// query on 1024 slots 13, 18, 24 us; 64 on 8192 33, 32, 39; 2 x 99 on 512 24,
+// 19, 19 (uncut: 19).
 struct PromptPlan {
   int64_t tiles, items;  // per (b, g) row; of all rows and parts
   int splits;
@@ -353,9 +365,15 @@ fasa_status fasa_attend_prompt(const fasa_cache* c, const fasa_paged* pg, const 
   SpanParams p{};
   span_fill(p, c, pg, sp, q, out, n_q);
   if (c->dtype == FASA_F32 && span_tiled(p, d)) return launch_tile(p, stream);
-  // tokens share a CTA up to 8 query rows, while that leaves every SM two CTAs
+  // Tokens share a CTA, up to 8 query rows, while there are more CTAs than run
+  // at once (two per SM): a CTA of more rows takes longer (one, two, four, eight
+  // rows 44, 50, 64, 81 us over 1000 float32 slots), a second round takes as
+  // long again. 8/8 heads, apart and shared: 32 tokens 44, 81 us; 64 tokens 83,
+  // 51; 150 tokens 184, 85. Over the host link the reads are what counts: always
+  // (8/8 heads, 1000 bf16 slots: 2 tokens 410, 387 us; 8 tokens 675, 377).
   const int64_t rows = (int64_t)c->batch * c->n_kv_heads;
-  while (2 * p.tokens * p.group <= 8 && ceil_div(n_q, 2 * p.tokens) * rows >= 2LL * d.sms) p.tokens *= 2;
+  const bool host = host_resident(c->k) || host_resident(c->v);
+  while (2 * p.tokens * p.group <= 8 && (host || ceil_div(n_q, p.tokens) * rows > 2LL * d.sms)) p.tokens *= 2;
   const dim3 grid((unsigned)ceil_div(n_q, p.tokens), (unsigned)rows, 1);
   return span_cc_launch(p, c->dtype, grid, stream);
 }
