@@ -150,15 +150,16 @@ def _stream(stream) -> int | None:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _new(stream, device, make, returned=False):
-    """make(), a tensor for a call that launches on `stream`. The allocator
-    hands a freed block out again in the order of the stream that was current
-    when it was allocated, so the launch stream is made current: the block is
-    neither still in use by another stream's work nor reused under the launch.
-    A tensor that goes back to the caller is also kept from reuse until what
-    the caller's own stream does with it is done."""
+def _new(stream, near, make, returned=False):
+    """make(), a tensor for a call that launches on `stream` of tensor near's
+    device. The allocator hands a freed block out again in the order of the
+    stream that was current when it was allocated, so the launch stream is made
+    current: the block is neither still in use by another stream's work nor
+    reused under the launch. A tensor that goes back to the caller is also kept
+    from reuse until what the caller's own stream does with it is done."""
     if stream is None:
         return make()
+    device = near.device
     current = torch.cuda.current_stream(device)
     handle = _stream(stream)
     if handle == current.cuda_stream:
@@ -176,9 +177,13 @@ def _ptr(t: torch.Tensor | None):
     return None if t is None else t.data_ptr()
 
 
-def _dev(t: torch.Tensor, name: str, dtype=None):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
+def _dev(t: torch.Tensor, name: str, dtype=None, home=None):
+    """t, a contiguous CUDA tensor of this dtype, on device `home` if given."""
+    if home is None or not isinstance(t, torch.Tensor) or t.get_device() != home:
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA tensor")
+        if home is not None:
+            raise ValueError(f"{name} must be on the cache's device {home}, got {t.get_device()}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
@@ -318,13 +323,13 @@ def fasa_decode_paged(cache: PagedKVCache, seq_len, q, max_seq_len: int, max_bud
     _q(cache, q)
     vl = _varlen(seq_len, budget, max_seq_len, max_budget, q_prerotated)
     if out is None:
-        out = _new(stream, q.device, lambda: torch.empty_like(q), True)
+        out = _new(stream, q, lambda: torch.empty_like(q), True)
     _dev(out, "out", cache.dtype)
     if idx_out is not None:
         _dev(idx_out, "idx_out", torch.int32)
     if workspace is None:
         need = int(lib().fasa_decode_paged_workspace_bytes(cache.ref(), cache.pref(), ctypes.byref(vl)))
-        workspace = _new(stream, q.device, lambda: torch.zeros(max(need, 1), dtype=torch.uint8, device=q.device))
+        workspace = _new(stream, q, lambda: torch.zeros(max(need, 1), dtype=torch.uint8, device=q.device))
     _dev(workspace, "workspace", torch.uint8)
     _check(lib().fasa_decode_paged(cache.ref(), cache.pref(), ctypes.byref(vl), q.data_ptr(), out.data_ptr(),
                                    _ptr(idx_out), workspace.data_ptr(), workspace.numel(), _stream(stream)),
@@ -344,8 +349,8 @@ def fasa_append_kv(cache: KVCache, k_new, v_new, pos0: int, stream=None) -> None
                                 _stream(stream)), "fasa_append_kv")
 
 
-def _q(cache, q):
-    _dev(q, "q", cache.dtype)
+def _q(cache, q, home=None):
+    _dev(q, "q", cache.dtype, home)
     if tuple(q.shape) != (cache.batch, cache.n_q_heads, HEAD_DIM):
         raise ValueError("q must be [B, Hq, 128]")
     return q
@@ -354,7 +359,7 @@ def _q(cache, q):
 def fasa_score(cache: KVCache, length: int, q, q_pos: int, scores=None, stream=None):
     _q(cache, q)
     if scores is None:
-        scores = _new(stream, q.device, lambda: torch.empty(cache.batch, cache.n_kv_heads, length, dtype=torch.float32,
+        scores = _new(stream, q, lambda: torch.empty(cache.batch, cache.n_kv_heads, length, dtype=torch.float32,
                                                             device=q.device), True)
     _dev(scores, "scores", torch.float32)
     _check(lib().fasa_score(cache.ref(), length, q.data_ptr(), q_pos, scores.data_ptr(), _stream(stream)),
@@ -368,7 +373,7 @@ def fasa_select_topk(scores, k: int, idx=None, stream=None):
     rows = scores.numel() // max(length, 1)
     k_eff = min(k, length)
     if idx is None:
-        idx = _new(stream, scores.device, lambda: torch.empty(*scores.shape[:-1], k_eff, dtype=torch.int32,
+        idx = _new(stream, scores, lambda: torch.empty(*scores.shape[:-1], k_eff, dtype=torch.int32,
                                                               device=scores.device), True)
     _dev(idx, "idx", torch.int32)
     _check(lib().fasa_select_topk(scores.data_ptr(), rows, length, k, idx.data_ptr(), _stream(stream)),
@@ -380,7 +385,7 @@ def fasa_sparse_attend(cache: KVCache, length: int, q, q_pos: int, idx, out=None
     _q(cache, q)
     _dev(idx, "idx", torch.int32)
     if out is None:
-        out = _new(stream, q.device, lambda: torch.empty_like(q), True)
+        out = _new(stream, q, lambda: torch.empty_like(q), True)
     _dev(out, "out", cache.dtype)
     _check(lib().fasa_sparse_attend(cache.ref(), length, q.data_ptr(), q_pos, idx.data_ptr(), idx.shape[-1],
                                     out.data_ptr(), _stream(stream)), "fasa_sparse_attend")
@@ -404,13 +409,13 @@ def fasa_decode(cache: KVCache, length: int, q, q_pos: int, k: int, out=None, id
     given workspace must have been zeroed once (fasa_decode_workspace)."""
     _q(cache, q)
     if out is None:
-        out = _new(stream, q.device, lambda: torch.empty_like(q), True)
+        out = _new(stream, q, lambda: torch.empty_like(q), True)
     _dev(out, "out", cache.dtype)
     if idx_out is not None:
         _dev(idx_out, "idx_out", torch.int32)
     need = fasa_decode_workspace_bytes(cache, length, k)
     if workspace is None:
-        workspace = _new(stream, q.device, lambda: torch.zeros(max(need, 1), dtype=torch.uint8, device=q.device))
+        workspace = _new(stream, q, lambda: torch.zeros(max(need, 1), dtype=torch.uint8, device=q.device))
     _dev(workspace, "workspace", torch.uint8)
     _check(lib().fasa_decode(cache.ref(), length, q.data_ptr(), q_pos, k, out.data_ptr(), _ptr(idx_out),
                              workspace.data_ptr(), workspace.numel(), _stream(stream)), "fasa_decode")
@@ -451,12 +456,12 @@ def fasa_decode_varlen(cache: KVCache, seq_len, q, max_seq_len: int, max_budget:
     _q(cache, q)
     vl = _varlen(seq_len, budget, max_seq_len, max_budget, q_prerotated)
     if out is None:
-        out = _new(stream, q.device, lambda: torch.empty_like(q), True)
+        out = _new(stream, q, lambda: torch.empty_like(q), True)
     _dev(out, "out", cache.dtype)
     if idx_out is not None:
         _dev(idx_out, "idx_out", torch.int32)
     if workspace is None:
-        workspace = _new(stream, q.device,
+        workspace = _new(stream, q,
                          lambda: fasa_decode_varlen_workspace(cache, max_seq_len, max_budget, q.device))
     _dev(workspace, "workspace", torch.uint8)
     _check(lib().fasa_decode_varlen(cache.ref(), ctypes.byref(vl), q.data_ptr(), out.data_ptr(), _ptr(idx_out),
@@ -481,12 +486,12 @@ def fasa_decode_multi(cache: KVCache, length: int, q, q_pos0: int, k: int, out=N
         raise ValueError("q must be [B, n_q, Hq, 128]")
     n_q = q.shape[1]
     if out is None:
-        out = _new(stream, q.device, lambda: torch.empty_like(q), True)
+        out = _new(stream, q, lambda: torch.empty_like(q), True)
     _dev(out, "out", cache.dtype)
     if idx_out is not None:
         _dev(idx_out, "idx_out", torch.int32)
     if workspace is None:
-        workspace = _new(stream, q.device, lambda: fasa_decode_multi_workspace(cache, length, n_q, k, q.device))
+        workspace = _new(stream, q, lambda: fasa_decode_multi_workspace(cache, length, n_q, k, q.device))
     _dev(workspace, "workspace", torch.uint8)
     _check(lib().fasa_decode_multi(cache.ref(), length, q.data_ptr(), q_pos0, n_q, k, out.data_ptr(),
                                    _ptr(idx_out), workspace.data_ptr(), workspace.numel(), _stream(stream)),
@@ -508,12 +513,9 @@ def _launch(name, t, stream, *args) -> None:
         _check(status, name)
 
 
-def _home(cache, **tensors):
-    """Every given tensor lies on the cache's device: the kernels read both."""
-    dev = cache.sketch.get_device()
-    for name, t in tensors.items():
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"{name} must be on the cache's device ({cache.sketch.device}), got {t.device}")
+def _home(cache):
+    """The cache's device, where everything that its kernels read lies too."""
+    return cache.sketch.get_device()
 
 
 def _pages(cache):
@@ -521,33 +523,33 @@ def _pages(cache):
     return cache.pref() if isinstance(cache, PagedKVCache) else None
 
 
-def _per_seq(cache, t, name):
+def _per_seq(cache, t, name, home=None):
     """Address of an int32 [B] device tensor, or None."""
     if t is None:
         return None
-    _dev(t, name, torch.int32)
+    _dev(t, name, torch.int32, home)
     if t.numel() != cache.batch:
         raise ValueError(f"{name} must have one value per sequence ({cache.batch}), got {t.numel()}")
     return t.data_ptr()
 
 
-def _per_slot(cache, t, name, dtype):
+def _per_slot(cache, t, name, dtype, home=None):
     """Address of a [B, Hkv, max_len] device tensor, or None."""
     if t is None:
         return None
-    _dev(t, name, dtype)
+    _dev(t, name, dtype, home)
     if tuple(t.shape) != (cache.batch, cache.n_kv_heads, cache.max_len):
         raise ValueError(f"{name} must be [B, Hkv, max_len] = "
                          f"{[cache.batch, cache.n_kv_heads, cache.max_len]}, got {list(t.shape)}")
     return t.data_ptr()
 
 
-def _span(cache, seq_len, max_seq_len, window, n_sink, q_pos, q_len, q_prerotated):
+def _span(cache, seq_len, max_seq_len, window, n_sink, q_pos, q_len, q_prerotated, home=None):
     if seq_len is None:
         raise TypeError("seq_len must be a CUDA tensor")
-    return fasa_span(_per_seq(cache, seq_len, "seq_len"),
-                     None if q_pos is None else _per_seq(cache, q_pos, "q_pos"),
-                     None if q_len is None else _per_seq(cache, q_len, "q_len"),
+    return fasa_span(_per_seq(cache, seq_len, "seq_len", home),
+                     None if q_pos is None else _per_seq(cache, q_pos, "q_pos", home),
+                     None if q_len is None else _per_seq(cache, q_len, "q_len", home),
                      int(max_seq_len), int(window), int(n_sink), 1 if q_prerotated else 0)
 
 
@@ -578,19 +580,26 @@ def fasa_attend_decode(cache, seq_len, q, max_seq_len: int, window: int = 0, n_s
     device. mass, when given, is float32 [B, Hkv, max_len]: every visible
     slot's attention weight, summed over the group's heads, is added to it
     (prompts add none)."""
-    _q(cache, q)
-    sp = _span(cache, seq_len, max_seq_len, window, n_sink, q_pos, None, q_prerotated)
-    if out is None:
-        out = _new(stream, q.device, lambda: torch.empty_like(q), True)
-    _same(_dev(out, "out", cache.dtype), q)
-    m = _per_slot(cache, mass, "mass", torch.float32)
+    home = _home(cache)
+    _q(cache, q, home)
+    sp = _span(cache, seq_len, max_seq_len, window, n_sink, q_pos, None, q_prerotated, home)
+    m = _per_slot(cache, mass, "mass", torch.float32, home)
+    out = _out(cache, q, out, stream, home)
     if workspace is None:
-        workspace = _new(stream, q.device,
+        workspace = _new(stream, q,
                          lambda: fasa_attend_decode_workspace(cache, max_seq_len, mass is not None, q.device))
-    _dev(workspace, "workspace", torch.uint8)
-    _home(cache, q=q, seq_len=seq_len, q_pos=q_pos, mass=mass, out=out, workspace=workspace)
+    else:
+        _dev(workspace, "workspace", torch.uint8, home)
     _launch("fasa_attend_decode", q, stream, cache.ref(), _pages(cache), ctypes.byref(sp), q.data_ptr(),
             out.data_ptr(), m, workspace.data_ptr(), workspace.numel())
+    return out
+
+
+def _out(cache, q, out, stream, home):
+    """The given output, or a new one."""
+    if out is None:
+        return _new(stream, q, lambda: torch.empty_like(q), True)
+    _same(_dev(out, "out", cache.dtype, home), q)
     return out
 
 
@@ -614,27 +623,26 @@ def fasa_attend_prompt(cache, seq_len, q, max_seq_len: int, window: int = 0, n_s
     query j of sequence b at position q_pos[b] + j (default: the queries are
     the sequence's last tokens). With q_len (int32 [B] on the device) sequence
     b has q_len[b] queries; the other rows of out are left as they are."""
-    _dev(q, "q", cache.dtype)
+    home = _home(cache)
+    _dev(q, "q", cache.dtype, home)
     if q.dim() != 4 or tuple(q.shape[::2]) != (cache.batch, cache.n_q_heads) or q.shape[3] != HEAD_DIM:
         raise ValueError("q must be [B, n_q, Hq, 128]")
     n_q = q.shape[1]
-    sp = _span(cache, seq_len, max_seq_len, window, n_sink, q_pos, q_len, q_prerotated)
-    if out is None:
-        out = _new(stream, q.device, lambda: torch.empty_like(q), True)
-    _same(_dev(out, "out", cache.dtype), q)
+    sp = _span(cache, seq_len, max_seq_len, window, n_sink, q_pos, q_len, q_prerotated, home)
+    out = _out(cache, q, out, stream, home)
     if workspace is None:
-        workspace = _new(stream, q.device, lambda: fasa_attend_prompt_workspace(cache, n_q, max_seq_len, q.device))
-    _dev(workspace, "workspace", torch.uint8)
-    _home(cache, q=q, seq_len=seq_len, q_pos=q_pos, q_len=q_len, out=out, workspace=workspace)
+        workspace = _new(stream, q, lambda: fasa_attend_prompt_workspace(cache, n_q, max_seq_len, q.device))
+    else:
+        _dev(workspace, "workspace", torch.uint8, home)
     _launch("fasa_attend_prompt", q, stream, cache.ref(), _pages(cache), ctypes.byref(sp), q.data_ptr(), n_q,
             out.data_ptr(), workspace.data_ptr(), workspace.numel())
     return out
 
 
-def _evict_desc(cache, seq_len, cur_pos, max_seq_len, budget, n_sink, n_recent):
+def _evict_desc(cache, seq_len, cur_pos, max_seq_len, budget, n_sink, n_recent, home=None):
     if seq_len is None or cur_pos is None:
         raise TypeError("seq_len and cur_pos must be CUDA tensors")
-    return fasa_evict_desc(_per_seq(cache, seq_len, "seq_len"), _per_seq(cache, cur_pos, "cur_pos"),
+    return fasa_evict_desc(_per_seq(cache, seq_len, "seq_len", home), _per_seq(cache, cur_pos, "cur_pos", home),
                            int(max_seq_len), int(budget), int(n_sink), int(n_recent))
 
 
@@ -655,22 +663,21 @@ def fasa_evict(cache, seq_len, cur_pos, mass, slot_pos, max_seq_len: int, budget
     budget move into the holes before it. mass (float32) and slot_pos (int32)
     are [B, Hkv, max_len], updated in place unless mass_out / slot_pos_out are
     given. Returns the new lengths, int32 [B]."""
-    d = _evict_desc(cache, seq_len, cur_pos, max_seq_len, budget, n_sink, n_recent)
+    home = _home(cache)
+    d = _evict_desc(cache, seq_len, cur_pos, max_seq_len, budget, n_sink, n_recent, home)
     if mass is None or slot_pos is None:
         raise TypeError("mass and slot_pos must be CUDA tensors")
-    mp = _per_slot(cache, mass, "mass", torch.float32)
-    sp = _per_slot(cache, slot_pos, "slot_pos", torch.int32)
-    mo = mp if mass_out is None else _per_slot(cache, mass_out, "mass_out", torch.float32)
-    so = sp if slot_pos_out is None else _per_slot(cache, slot_pos_out, "slot_pos_out", torch.int32)
+    mp = _per_slot(cache, mass, "mass", torch.float32, home)
+    sp = _per_slot(cache, slot_pos, "slot_pos", torch.int32, home)
+    mo = mp if mass_out is None else _per_slot(cache, mass_out, "mass_out", torch.float32, home)
+    so = sp if slot_pos_out is None else _per_slot(cache, slot_pos_out, "slot_pos_out", torch.int32, home)
     if len_out is None:
-        len_out = _new(stream, seq_len.device, lambda: torch.empty_like(seq_len), True)
-    lo = _per_seq(cache, len_out, "len_out")
+        len_out = _new(stream, seq_len, lambda: torch.empty_like(seq_len), True)
+    lo = _per_seq(cache, len_out, "len_out", home)
     if workspace is None:
-        workspace = _new(stream, seq_len.device,
-                         lambda: fasa_evict_workspace(cache, max_seq_len, budget, seq_len.device))
-    _dev(workspace, "workspace", torch.uint8)
-    _home(cache, seq_len=seq_len, cur_pos=cur_pos, mass=mass, slot_pos=slot_pos, mass_out=mass_out,
-          slot_pos_out=slot_pos_out, len_out=len_out, workspace=workspace)
+        workspace = _new(stream, seq_len, lambda: fasa_evict_workspace(cache, max_seq_len, budget, seq_len.device))
+    else:
+        _dev(workspace, "workspace", torch.uint8, home)
     _launch("fasa_evict", seq_len, stream, cache.ref(), _pages(cache), ctypes.byref(d), mp, sp, mo, so, lo,
             workspace.data_ptr(), workspace.numel())
     return len_out
@@ -680,16 +687,17 @@ def fasa_append_kv_at(cache, k_new, v_new, slot0, pos0, slot_pos=None, mass=None
     """Append n_new tokens to every sequence b at slots slot0[b] .., rotated
     at positions pos0[b] .. (int32 [B] on the device). slot_pos (int32) and
     mass (float32), [B, Hkv, max_len], get the new slots' positions and zeros."""
-    _dev(k_new, "k_new", cache.dtype)
-    _dev(v_new, "v_new", cache.dtype)
+    home = _home(cache)
+    _dev(k_new, "k_new", cache.dtype, home)
+    _dev(v_new, "v_new", cache.dtype, home)
     n_new = k_new.shape[2]
     if tuple(k_new.shape) != (cache.batch, cache.n_kv_heads, n_new, HEAD_DIM) or v_new.shape != k_new.shape:
         raise ValueError("k_new, v_new must be [B, Hkv, n_new, 128]")
     if slot0 is None or pos0 is None:
         raise TypeError("slot0 and pos0 must be CUDA tensors")
-    s0, p0 = _per_seq(cache, slot0, "slot0"), _per_seq(cache, pos0, "pos0")
-    sp, m = _per_slot(cache, slot_pos, "slot_pos", torch.int32), _per_slot(cache, mass, "mass", torch.float32)
-    _home(cache, k_new=k_new, v_new=v_new, slot0=slot0, pos0=pos0, slot_pos=slot_pos, mass=mass)
+    s0, p0 = _per_seq(cache, slot0, "slot0", home), _per_seq(cache, pos0, "pos0", home)
+    sp = _per_slot(cache, slot_pos, "slot_pos", torch.int32, home)
+    m = _per_slot(cache, mass, "mass", torch.float32, home)
     _launch("fasa_append_kv_at", k_new, stream, cache.ref(), _pages(cache), k_new.data_ptr(), v_new.data_ptr(), n_new,
             s0, p0, sp, m)
 
@@ -730,10 +738,10 @@ def fasa_dense_decode(cache: KVCache, length: int, q, q_pos: int, out=None, work
     given workspace must have been zeroed once (fasa_dense_workspace)."""
     _q(cache, q)
     if out is None:
-        out = _new(stream, q.device, lambda: torch.empty_like(q), True)
+        out = _new(stream, q, lambda: torch.empty_like(q), True)
     _dev(out, "out", cache.dtype)
     if workspace is None:
-        workspace = _new(stream, q.device, lambda: fasa_dense_workspace(cache, length, q.device))
+        workspace = _new(stream, q, lambda: fasa_dense_workspace(cache, length, q.device))
     _dev(workspace, "workspace", torch.uint8)
     _check(lib().fasa_dense_decode(cache.ref(), length, q.data_ptr(), q_pos, out.data_ptr(), workspace.data_ptr(),
                                    workspace.numel(), _stream(stream)), "fasa_dense_decode")
@@ -767,7 +775,7 @@ def fasa_calibrate_scores(cache: KVCache, length: int, q_win, q_pos0: int, plane
     """Score planes [B, Hkv, n_win, 65, len] float32 of the calibration queries."""
     n_win = _q_win(cache, q_win)
     if planes is None:
-        planes = _new(stream, q_win.device,
+        planes = _new(stream, q_win,
                       lambda: torch.empty(cache.batch, cache.n_kv_heads, n_win, CAL_PLANES, length,
                                           dtype=torch.float32, device=q_win.device), True)
     _dev(planes, "planes", torch.float32)
@@ -784,12 +792,12 @@ def fasa_calibrate_counts(planes, n_kv_heads: int, budget: int, counts=None, wor
         raise ValueError("planes must be [..., n_win, 65, len]")
     rows = planes.numel() // (n_win * CAL_PLANES * length)
     if counts is None:
-        counts = _new(stream, planes.device,
+        counts = _new(stream, planes,
                       lambda: torch.empty(n_kv_heads, 64, dtype=torch.int32, device=planes.device), True)
     _dev(counts, "counts", torch.int32)
     need = rows * n_win * CAL_PLANES * min(budget, length) * 4
     if workspace is None:
-        workspace = _new(stream, planes.device,
+        workspace = _new(stream, planes,
                          lambda: torch.empty(max(need, 1), dtype=torch.uint8, device=planes.device))
     _dev(workspace, "workspace", torch.uint8)
     _check(lib().fasa_calibrate_counts(planes.data_ptr(), rows, n_kv_heads, n_win, length, budget,
@@ -802,7 +810,7 @@ def fasa_calibrate_dominant(counts, n_dom: int, dom_idx=None, stream=None):
     """I_dom [Hkv, n_dom] int32 from counts [Hkv, 64]."""
     _dev(counts, "counts", torch.int32)
     if dom_idx is None:
-        dom_idx = _new(stream, counts.device, lambda: torch.empty(counts.shape[0], n_dom, dtype=torch.int32,
+        dom_idx = _new(stream, counts, lambda: torch.empty(counts.shape[0], n_dom, dtype=torch.int32,
                                                                   device=counts.device), True)
     _dev(dom_idx, "dom_idx", torch.int32)
     _check(lib().fasa_calibrate_dominant(counts.data_ptr(), counts.shape[0], n_dom, dom_idx.data_ptr(),
@@ -816,14 +824,14 @@ def fasa_calibrate(cache: KVCache, length: int, q_win, q_pos0: int, budget: int,
     n_win = _q_win(cache, q_win)
     dev = q_win.device
     if counts is None:
-        counts = _new(stream, dev, lambda: torch.empty(cache.n_kv_heads, 64, dtype=torch.int32, device=dev), True)
+        counts = _new(stream, q_win, lambda: torch.empty(cache.n_kv_heads, 64, dtype=torch.int32, device=dev), True)
     if dom_idx is None:
-        dom_idx = _new(stream, dev, lambda: torch.empty(cache.n_kv_heads, n_dom, dtype=torch.int32, device=dev), True)
+        dom_idx = _new(stream, q_win, lambda: torch.empty(cache.n_kv_heads, n_dom, dtype=torch.int32, device=dev), True)
     _dev(counts, "counts", torch.int32)
     _dev(dom_idx, "dom_idx", torch.int32)
     need = fasa_calibrate_workspace_bytes(cache, length, n_win, budget)
     if workspace is None:
-        workspace = _new(stream, dev, lambda: torch.empty(max(need, 1), dtype=torch.uint8, device=dev))
+        workspace = _new(stream, q_win, lambda: torch.empty(max(need, 1), dtype=torch.uint8, device=dev))
     _dev(workspace, "workspace", torch.uint8)
     _check(lib().fasa_calibrate(cache.ref(), length, q_win.data_ptr(), q_pos0, n_win, budget, n_dom,
                                 counts.data_ptr(), dom_idx.data_ptr(), workspace.data_ptr(), workspace.numel(),

@@ -4,14 +4,28 @@ import pytest
 import torch
 
 from rope_frequency_chunk_b200 import fasa as F
-from tests.test_binding_streams import B, HKV, HQ, N, C, FakeLib, i32, q
+from tests.test_binding_streams import B, HKV, HQ, N, Cache, FakeLib, i32, q
 
 U8 = torch.uint8
 
 
-class Elsewhere(torch.Tensor):
+class Here(torch.Tensor):
+    is_cuda = True
+
+    def get_device(self):
+        return 0
+
+
+class Elsewhere(Here):
     def get_device(self):
         return 5
+
+
+class CacheHere(Cache):
+    sketch = torch.zeros(1).as_subclass(Here)
+
+
+C = CacheHere()
 
 
 def slots(dtype=torch.float32):
@@ -42,8 +56,8 @@ def test_tensors_elsewhere_are_refused(monkeypatch, name):
     call, args = CALLS[name]
     launched = []
     monkeypatch.setattr(F, "_lib", FakeLib())
-    monkeypatch.setattr(F, "_dev", lambda t, name, dtype=None: t)
     monkeypatch.setattr(F, "_launch", lambda name, *a: launched.append(name))
+    args = {k: t.as_subclass(Here) for k, t in args.items()}
     call(**args)
     assert launched == ["fasa_" + name]
     for k, t in args.items():

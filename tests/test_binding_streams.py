@@ -87,7 +87,7 @@ def made(monkeypatch):
         return g
 
     monkeypatch.setattr(F, "_lib", FakeLib())
-    monkeypatch.setattr(F, "_dev", lambda t, name, dtype=None: t)
+    monkeypatch.setattr(F, "_dev", lambda t, name, dtype=None, home=None: t)
     monkeypatch.setattr(F, "_stream", lambda s: now[-1] if s is None else getattr(s, "cuda_stream", s))
     monkeypatch.setattr(F, "_launch", lambda *a: None, raising=False)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Stream(now[-1]))
