@@ -420,32 +420,31 @@ __device__ __forceinline__ float pr_top(const uint32_t* s, int n) {
 constexpr float kPrScale = 1.4426950408889634f * 0.08838834764831845f;  // log2(e) / sqrt(128)
 
 // The two warps of a row quadrant meet at a named barrier. A warp whose wait
-// for the tensor core gave up still comes, having raised the block's `failed`,
-// and both leave together. The barrier itself carries the vote: read behind
-// it, the word could be raised (by any warp of the block) between the two
-// warps' reads, and the one that stayed would wait at the barrier for good.
+// for the tensor core gave up still comes, and both leave together: the barrier
+// itself tells both whether either gave up. (Read from a word in shared memory
+// behind the barrier, the answers could differ, and the warp that stayed would
+// wait at the barrier for good.)
 struct PrPair {
   int id;                 // barrier 1 .. 8
-  volatile int* failed;   // one word for the block
   volatile float* mine;   // this thread's slot, the other thread's
   volatile float* other;
 };
-// False, to both warps, once either of them has seen `failed` raised.
-__device__ __forceinline__ bool pr_meet(const PrPair& pr) {
-  uint32_t gone;
+// Clears ok of both warps if either comes without it.
+__device__ __forceinline__ void pr_meet(const PrPair& pr, bool& ok) {
+  uint32_t all;
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.s32 q, %2, 0;\n barrier.cta.red.or.pred p, %1, 64, q;\n"
+      "{\n .reg .pred p, q;\n setp.ne.u32 q, %2, 0;\n barrier.cta.red.and.pred p, %1, 64, q;\n"
       " selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(gone)
-      : "r"(pr.id), "r"(*pr.failed)
+      : "=r"(all)
+      : "r"(pr.id), "r"((uint32_t)ok)
       : "memory");
-  return gone == 0;
+  ok = all != 0;
 }
 // The larger of the two threads' values. The slots are free again once both
 // warps have handed over P, before the next S.
 __device__ __forceinline__ float pr_join(float x, const PrPair& pr, bool& ok) {
   *pr.mine = x;
-  ok = pr_meet(pr);
+  pr_meet(pr, ok);
   return pr_max(x, *pr.other);
 }
 
@@ -454,15 +453,15 @@ __device__ __forceinline__ float pr_join(float x, const PrPair& pr, bool& ok) {
 // read a second time for the exponentials: keeping all 64 over the exchange of
 // the maxima costs the 104 registers some spills (492 against 463 us for a
 // causal prompt of 8192 tokens).
-__device__ __forceinline__ bool pr_softmax_whole(PrRow& row, uint32_t t_s, uint32_t t_o, bool first, const PrPair& pr) {
+__device__ __forceinline__ void pr_softmax_whole(PrRow& row, uint32_t t_s, uint32_t t_o, bool first, const PrPair& pr,
+                                                 bool& ok) {
   uint32_t a[32], b[32], pk[16];
   pr_ld32(t_s, b);
   pr_ld32(t_s + 32, a);
   pr_ld_wait(b);
   pr_ld_wait(a);
-  bool ok;
   const float top = pr_join(pr_max(pr_top(b, 32), pr_top(a, 32)), pr, ok);
-  if (!ok) return false;
+  if (!ok) return;
   pr_follow(row, top * kPrScale, t_o, first);
   const float off = row.m_ref == -INFINITY ? 0.0f : -row.m_ref;
   const uint64_t c2 = pr_two(kPrScale, kPrScale), off2 = pr_two(off, off);
@@ -475,14 +474,13 @@ __device__ __forceinline__ bool pr_softmax_whole(PrRow& row, uint32_t t_s, uint3
   pr_st16(t_s + kPrP, pk);
   const float2 y = pr_both(pr_add2(ls[0], ls[1]));
   row.l += y.x + y.y;
-  return true;
 }
 
 // The same under the rows' masks, for those of the half's two 32-column
 // chunks (c0, c0 + 1) that lie in [ca, cb). bad: the block's pages outside the
 // pool.
-__device__ __forceinline__ bool pr_softmax_part(PrRow& row, uint32_t t_s, uint32_t t_o, int t0, int c0, int ca, int cb,
-                                                bool first, unsigned bad, int log2bs, const PrPair& pr) {
+__device__ __forceinline__ void pr_softmax_part(PrRow& row, uint32_t t_s, uint32_t t_o, int t0, int c0, int ca, int cb,
+                                                bool first, unsigned bad, int log2bs, const PrPair& pr, bool& ok) {
   uint32_t s[32], ms[2];
   float mx = -INFINITY;
   auto hide = [&](int q) {
@@ -503,9 +501,8 @@ __device__ __forceinline__ bool pr_softmax_part(PrRow& row, uint32_t t_s, uint32
     hide(q);
     mx = pr_max(mx, pr_top(s, 32));
   }
-  bool ok;
   const float top = pr_join(mx, pr, ok);
-  if (!ok) return false;
+  if (!ok) return;
   pr_follow(row, top * kPrScale, t_o, first);
   const float off = row.m_ref == -INFINITY ? 0.0f : -row.m_ref;
   const uint64_t c2 = pr_two(kPrScale, kPrScale), off2 = pr_two(off, off);
@@ -523,7 +520,6 @@ __device__ __forceinline__ bool pr_softmax_part(PrRow& row, uint32_t t_s, uint32
   }
   const float2 y = pr_both(pr_add2(ls[0], ls[1]));
   row.l += y.x + y.y;
-  return true;
 }
 
 template <int TERMS>
@@ -540,7 +536,6 @@ __global__ void __launch_bounds__(kPrThreads, 1) span_prompt_kernel(const __grid
   uint64_t* bar_q = bar_o + 2;        // [2] an item's Q is staged
   uint64_t* bar_f = bar_q + 2;        // [2] an item's Q is no longer read
   uint32_t* tbase_s = reinterpret_cast<uint32_t*>(bar_f + 2);
-  volatile int* failed = reinterpret_cast<int*>(tbase_s + 1);
   double* turns = reinterpret_cast<double*>(smem + SM::kTurns);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = p.s.group, hq = p.s.n_kv_heads * G, tt = pr_tokens(G);
@@ -561,7 +556,6 @@ __global__ void __launch_bounds__(kPrThreads, 1) span_prompt_kernel(const __grid
       mbar_init(bar_q + i, TERMS == 1 ? 1 : 8);
       mbar_init(bar_f + i, 1);
     }
-    *failed = 0;
     fence_mbar_init();
   }
   if (warp == 16) tc_alloc(tbase_s, 512);
@@ -587,11 +581,9 @@ __global__ void __launch_bounds__(kPrThreads, 1) span_prompt_kernel(const __grid
     const uint32_t t_s = tbase + sub * 128 + half * 64 + lanes, t_o = tbase + 256 + sub * 128 + half * 64 + lanes;
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.s.out);
     float* pair = reinterpret_cast<float*>(smem + SM::kPair) + sub * 256;
-    const PrPair pr{1 + sub * 4 + (warp & 3), failed, pair + half * 128 + r, pair + (half ^ 1) * 128 + r};
-    // a bounded wait; a warp that gave up goes on to the next meeting
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-      if (!pr_wait(bar, parity)) *failed = 1;
-    };
+    const PrPair pr{1 + sub * 4 + (warp & 3), pair + half * 128 + r, pair + (half ^ 1) * 128 + r};
+    bool ok = true;  // of this warp; one whose bounded wait gave up goes on to the next meeting
+    auto wait = [&](uint64_t* bar, uint32_t parity) { ok = pr_wait(bar, parity); };
     auto part_of = [&](const PrItem& w) {
       return p.part + (((int64_t)(w.b * p.s.n_kv_heads + w.g) * p.tiles_max + w.tile) * p.splits + w.split) * kPrPart;
     };
@@ -661,7 +653,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) span_prompt_kernel(const __grid
     uint32_t n_s = 0, n_o = 0;  // barrier phases used
     int it = 0;
     PrItem w;
-    bool more = next(it, w), ok = true;
+    bool more = next(it, w);
     if (TERMS == 2 && more && sub * tt < w.n_tok) stage_q(w);
     const int n_pg = p.s.pm.table ? max(1, kPrBlock >> p.s.pm.log2bs) : 0;
     while (more && ok) {
@@ -689,12 +681,12 @@ __global__ void __launch_bounds__(kPrThreads, 1) span_prompt_kernel(const __grid
           wait(bar_s + sub, n_s++ & 1);
           tc_fence_after();
           if (i >= f0 && i < f1 && !bad) {
-            ok = pr_softmax_whole(row, t_s, t_o, i == w.i0, pr);
+            pr_softmax_whole(row, t_s, t_o, i == w.i0, pr, ok);
           } else {
             const int t0 = w.u.unit(i) * kPrBlock;
             int ca, cb;
             pr_chunks(w.all, t0, ca, cb);
-            ok = pr_softmax_part(row, t_s, t_o, t0, half * 2, ca, cb, i == w.i0, bad, p.s.pm.log2bs, pr);
+            pr_softmax_part(row, t_s, t_o, t0, half * 2, ca, cb, i == w.i0, bad, p.s.pm.log2bs, pr, ok);
           }
           if (!ok) break;
           pr_stored(bar_p + sub, lane);
@@ -711,9 +703,9 @@ __global__ void __launch_bounds__(kPrThreads, 1) span_prompt_kernel(const __grid
       tc_fence_after();
       // the row's sum, once both threads are past their last exchange
       *pr.mine = row.l;
-      ok = pr_meet(pr);
+      pr_meet(pr, ok);
       const float l = row.l + *pr.other;
-      if (!pr_meet(pr)) ok = false;  // the slots are free again
+      pr_meet(pr, ok);  // the slots are free again
       if (!ok) break;
       if (p.splits == 1) {
         // rows of the lane's group of four: lane k stores the k-th 16 bytes
