@@ -565,7 +565,7 @@ size_t fasa_attend_decode_workspace_bytes(const fasa_cache* cache, const fasa_sp
  *  q_pos   : span->q_pos, or NULL: the query of sequence b sits at position
  *            seq_len[b], as in fasa_decode_varlen. span->q_len is not read.
  *  q       : [B][Hq][128] dtype.
- *  out     : [B][Hq][128] dtype.
+ *  out     : [B][Hq][128] dtype; may be q.
  *  mass    : nullable; [B][Hkv][max_len] float32. Each visible slot's
  *            attention weight, summed over the group's query heads, is added
  *            to it: mass[b][g][t] += sum_h softmax_t(...). Other slots are left
@@ -601,8 +601,8 @@ size_t fasa_attend_prompt_workspace_bytes(const fasa_cache* cache, const fasa_sp
  *  q_pos   : query j of sequence b sits at position q_pos[b] + j; NULL: the
  *            queries are the sequence's last tokens, q_pos[b] = seq_len[b] -
  *            q_len[b].
- *  q, out  : [B][n_q][Hq][128] dtype; rows j >= q_len[b] are not read and their
- *            output is left as it is.
+ *  q, out  : [B][n_q][Hq][128] dtype; rows j >= q_len[b] are not used and their
+ *            output is left as it is. out may be q.
  *  workspace : at least fasa_attend_prompt_workspace_bytes bytes, 256-byte
  *            aligned, as for fasa_attend_decode.
  *  Arithmetic: as fasa_attend_decode, but the probabilities of bf16 caches

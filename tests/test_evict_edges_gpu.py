@@ -141,3 +141,23 @@ def test_rows_and_moves_at_the_limits_of_one_launch(B, hkv, L, budget):
             assert torch.equal(m[b, g, :budget], m0[b, g, s]) and torch.equal(pos[b, g, :budget], p0[b, g, s])
             for x, was in zip((c.k, c.v, c.sketch), old[b]):
                 assert torch.equal(f.rows(x, b, budget)[g], was[g, s])
+
+
+@pytest.mark.parametrize("budget", [8192, 300000])
+def test_the_longest_row(budget):
+    """524288 slots, sixteen CTAs of 32768 each."""
+    L = 1 << 19
+    f = S.Filled([L, L - 5], 1, 1, BF, cap=L, n_dom=1)
+    c = f.cache
+    m = torch.rand(2, 1, L, generator=f.g, device=S.DEV).pow_(20)
+    m[1] = (m[1] * 4).floor()  # ties
+    pos = torch.argsort(torch.rand(2, 1, L, generator=f.g, device=S.DEV), -1).int()
+    old = [x.clone() for x in (c.k, c.v, c.sketch)]
+    m0, p0 = m.clone(), pos.clone()
+    F.fasa_evict(c, f.seq_len, f.seq_len - 1, m, pos, L, budget, n_sink=4, n_recent=256)
+    for b in range(2):
+        src = kept_order(m0[b, 0].cpu().numpy(), p0[b, 0].cpu().numpy(), f.lens[b], f.lens[b] - 1, budget, 4, 256)
+        s = torch.from_numpy(src).to(S.DEV)
+        assert torch.equal(m[b, 0, :budget], m0[b, 0, s]) and torch.equal(pos[b, 0, :budget], p0[b, 0, s])
+        for x, was in zip((c.k, c.v, c.sketch), old):
+            assert torch.equal(x[b, 0, :budget], was[b, 0, s])

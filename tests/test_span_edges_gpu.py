@@ -140,3 +140,67 @@ def test_f32_prompts_on_host_resident_caches(n_q):
     out = F.fasa_attend_prompt(c, f.seq_len, q, 800, window=300, n_sink=3)
     ref, _, size, z = S.attend64(f, 0, q[0], list(range(790 - n_q, 790)), 300, 3, False)
     S.check_out(out[0], ref, size, z, 790)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("prerot", [False, True])
+def test_outputs_may_take_the_queries_place(dtype, prerot):
+    """A row's queries are read before its output is written, whichever kernel
+    and however many blocks share it."""
+    f = S.Filled([3000, 70, 900], 8, 2, dtype, 16)
+    for n_q in (0, 1, 5, 60, 400):  # 0: the decode
+        q = (S.randn(f.g, 3, n_q, 8, 128) * 1.5 if n_q else S.randn(f.g, 3, 8, 128)).to(dtype)
+        call = F.fasa_attend_prompt if n_q else F.fasa_attend_decode
+        ref = call(f.cache, f.seq_len, q, 3000, q_prerotated=prerot)
+        assert torch.equal(call(f.cache, f.seq_len, q, 3000, q_prerotated=prerot, out=q), ref)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_the_most_rows(dtype):
+    """8191 sequences of 8 KV heads, the largest batch there is: append,
+    decode with weights, a prompt, an eviction, against float64."""
+    B, hkv, L, n = 8191, 8, 12, 3
+    g = torch.Generator(S.DEV).manual_seed(2)
+    c = F.KVCache(B, 2 * hkv, hkv, 1, L, dtype, S.BASE, [[i] for i in range(hkv)])
+    lens = torch.randint(0, L - n + 1, (B,), generator=g, device=S.DEV).int()
+    pos = torch.zeros(B, hkv, L, dtype=torch.int32, device=S.DEV)
+    mass = torch.zeros(B, hkv, L, device=S.DEV)
+    k, v = (S.randn(g, B, hkv, L - n, 128).to(dtype) for _ in range(2))
+    F.fasa_append_kv_at(c, k, v, torch.zeros_like(lens), torch.zeros_like(lens), slot_pos=pos, mass=mass)
+    k, v = (S.randn(g, B, hkv, n, 128).to(dtype) for _ in range(2))
+    F.fasa_append_kv_at(c, k, v, lens, lens, slot_pos=pos, mass=mass)
+    seq_len = lens + n
+    q = (S.randn(g, B, 2 * hkv, 128) * 1.5).to(dtype)
+    out = F.fasa_attend_decode(c, seq_len, q, L, mass=mass)
+    outp = F.fasa_attend_prompt(c, seq_len, q[:, None].contiguous(), L, q_pos=seq_len)
+    p = seq_len.double()[:, None, None] * S.BASE ** (-2.0 * torch.arange(64, dtype=torch.float64, device=S.DEV) / 128)
+    x0, x1 = q.double().split(64, -1)
+    x = torch.cat([x0 * p.cos() - x1 * p.sin(), x1 * p.cos() + x0 * p.sin()], -1).view(B, hkv, 2, 128)
+    kk, vv = c.k.double(), c.v.double()
+    see = (torch.arange(L, device=S.DEV) < seq_len[:, None])[:, None, None]
+    kk, vv = (torch.where(see[:, :, 0, :, None], t, 0.0) for t in (kk, vv))
+    z = (x @ kk.transpose(-1, -2) / math.sqrt(128)).masked_fill(~see, -math.inf)
+    z_max = float((x.abs() @ kk.abs().transpose(-1, -2)).max()) / math.sqrt(128)
+    w = torch.softmax(z, -1)
+    ref, size = (w @ vv).view(B, 2 * hkv, 128), (w @ vv.abs()).view(B, 2 * hkv, 128)
+    S.check_out(out, ref, size, z_max, L)
+    S.check_out(outp[:, 0], ref, size, z_max, L, p_rel=2.0 ** -8)
+    want = w.sum(2)
+    rel = 2.0 * S.logit_error(dtype, z_max) + (L / 4 + 64) * 2.0 ** -24
+    assert ((mass.double() - want).abs() <= rel * want + 2.0 ** -24 * 3).all()
+    m0, k0 = mass.clone(), c.k.clone()
+    n_new = F.fasa_evict(c, seq_len, seq_len - 1, mass, pos, L, 4, n_recent=1)
+    assert torch.equal(n_new, seq_len.clamp(max=4))
+    # the kept weights: the newest slot's and the three largest others
+    last = (torch.arange(L, device=S.DEV) == seq_len[:, None] - 1)[:, None]
+    top = m0.masked_fill(last, -1.0).masked_fill(~see[:, :, 0], -1.0).sort(-1, descending=True).values[..., :3]
+    for L0 in (4, 9, 12):  # sequences of these lengths: their multisets of weights
+        b = seq_len == L0
+        got = mass[b][..., :4].sort(-1).values
+        want = torch.cat([top[b], m0[b][..., L0 - 1:L0]], -1).sort(-1).values
+        assert b.any() and torch.equal(got, want)
+    for i in range(4):  # and their keys went with them
+        t = pos[..., i].clamp(min=0).long()
+        moved = torch.gather(k0, 2, t[..., None, None].expand(-1, -1, 1, 128))[:, :, 0]
+        on = (i < n_new)[:, None].expand(-1, hkv)
+        assert torch.equal(c.k[:, :, i][on], moved[on])

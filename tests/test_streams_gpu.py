@@ -118,3 +118,31 @@ def test_fasa_decode_on_a_side_stream():
     scribble([F.fasa_decode_workspace_bytes(f.cache, 1500, 64), q.numel() * 2])
     torch.cuda.synchronize()
     assert torch.equal(out, ref)
+
+
+def test_a_side_stream_inside_a_capture():
+    """Calls on a forked stream of a captured graph: their scratch belongs to
+    the graph, and replays give the eager results."""
+    f = S.Filled([1200, 333], 8, 2, BF, 16)
+    q = (S.randn(f.g, 2, 8, 128) * 1.5).to(BF)
+    qp = (S.randn(f.g, 2, 5, 8, 128) * 1.5).to(BF)
+    ref = [F.fasa_attend_decode(f.cache, f.seq_len, q, 1200), F.fasa_attend_prompt(f.cache, f.seq_len, qp, 1200)]
+    outs = [torch.zeros_like(x) for x in ref]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        outs[1].copy_(F.fasa_attend_prompt(f.cache, f.seq_len, qp, 1200))
+        a = F.fasa_attend_decode(f.cache, f.seq_len, q, 1200, stream=side)
+        main.wait_stream(side)
+        outs[0].copy_(a)
+    del a
+    for _ in range(3):
+        for x in outs:
+            x.zero_()
+        scribble([1 << 20, 1 << 24])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], ref[0]) and torch.equal(outs[1], ref[1])
