@@ -369,11 +369,13 @@ fasa_status fasa_attend_prompt(const fasa_cache* c, const fasa_paged* pg, const 
   // at once (two per SM): a CTA of more rows takes longer (one, two, four, eight
   // rows 44, 50, 64, 81 us over 1000 float32 slots), a second round takes as
   // long again. 8/8 heads, apart and shared: 32 tokens 44, 81 us; 64 tokens 83,
-  // 51; 150 tokens 184, 85. Over the host link the reads are what counts: always
-  // (8/8 heads, 1000 bf16 slots: 2 tokens 410, 387 us; 8 tokens 675, 377).
+  // 51; 150 tokens 184, 85; one token of 64 sequences over 500 slots 57, 103.
+  // Over the host link the reads are what counts: always (8/8 heads, 1000 bf16
+  // slots: 2 tokens 392, 350 us; 8 tokens 675, 377; 40 tokens 3300, 470).
   const int64_t rows = (int64_t)c->batch * c->n_kv_heads;
   const bool host = host_resident(c->k) || host_resident(c->v);
-  while (2 * p.tokens * p.group <= 8 && (host || ceil_div(n_q, p.tokens) * rows > 2LL * d.sms)) p.tokens *= 2;
+  while (2 * p.tokens * p.group <= 8 && p.tokens < n_q && (host || ceil_div(n_q, p.tokens) * rows > 2LL * d.sms))
+    p.tokens *= 2;
   const dim3 grid((unsigned)ceil_div(n_q, p.tokens), (unsigned)rows, 1);
   return span_cc_launch(p, c->dtype, grid, stream);
 }
